@@ -31,7 +31,9 @@ EXPORTED = ("nvfp4_status_string", "nvfp4_version", "nvfp4_quantize", "nvfp4_ama
             "nvfp4_linear_noalloc", "nvfp4_linear_noalloc_max_bytes", "nvfp4_prepared_bytes", "nvfp4_prepare",
             "nvfp4_dequant_prepared", "nvfp4_linear_prepared_workspace_bytes", "nvfp4_linear_prepared",
             "nvfp4_stream_read", "nvfp4_stream_read_sink_words", "nvfp4_quantize_ws",
-            "nvfp4_quantize_workspace_bytes")
+            "nvfp4_quantize_workspace_bytes", "nvfp4_fp8_quantize", "nvfp4_rmsnorm_fp8", "nvfp4_silu_mul_fp8",
+            "nvfp4_fp8_linear_workspace_bytes", "nvfp4_fp8_linear", "nvfp4_fp8_linear_grouped_workspace_bytes",
+            "nvfp4_fp8_linear_grouped")
 
 
 class NVFP4Error(RuntimeError):
@@ -89,6 +91,13 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_linear_w4a4_workspace_bytes.argtypes = [i64, i64]
         L.nvfp4_linear_workspace_bytes.argtypes = [i64, i64, i64]
         L.nvfp4_linear_grouped_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nvfp4_fp8_quantize.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp]
+        L.nvfp4_rmsnorm_fp8.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, vp, vp, vp, vp]
+        L.nvfp4_silu_mul_fp8.argtypes = [vp, i64, i64, vp, vp, vp]
+        L.nvfp4_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nvfp4_fp8_linear.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_fp8_linear_grouped_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nvfp4_fp8_linear_grouped.argtypes = [vp, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
         for name in EXPORTED[2:]:
             getattr(L, name).restype = i64 if name.endswith(("_workspace_bytes", "_max_bytes", "_prepared_bytes", "_sink_words")) \
                 else i32
@@ -604,4 +613,202 @@ def linear_w4a4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, tsc
     _check(lib().nvfp4_linear_w4a4(x.data_ptr(), m, n, k, packed.data_ptr(), scales.data_ptr(), tscale.data_ptr(),
                                    out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(x)),
            "nvfp4_linear_w4a4")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# E4M3 tensors with an FP32 scale per 1 x 128 (activations) or 128 x 128
+# (weights) block.  Codes are uint8; torch.float8_e4m3fn tensors are taken too.
+# ---------------------------------------------------------------------------
+_FP8_BLOCK = 128
+_FP8_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _need_codes(t: torch.Tensor, name: str) -> None:
+    _need(t, torch.uint8 if t.dtype not in _FP8_CODES else t.dtype, name)
+
+
+def _call(fn, what: str, device: torch.device, *args) -> None:
+    """fn(*args, stream) on `device` and its current stream, whichever device is the current one."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+
+
+def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+def _fp8_blocks(n: int) -> int:
+    return -(-n // _FP8_BLOCK)
+
+
+def _fp8_k(k: int) -> None:
+    if k <= 0 or k % 16 != 0:
+        raise ValueError(f"the last dimension must be a positive multiple of 16, got {k}")
+
+
+def _fp8_outputs(lead, rows: int, k: int, block_rows: int, device: torch.device):
+    return (torch.empty((*lead, rows, k), dtype=torch.uint8, device=device),
+            torch.empty((*lead, -(-rows // block_rows), _fp8_blocks(k)), dtype=torch.float32, device=device))
+
+
+def fp8_quantize(w: torch.Tensor, block_rows: int = 1) -> Tuple[torch.Tensor, torch.Tensor]:
+    """BF16 [n, k] or [e, n, k] -> (codes uint8 of the same shape, scales float32 [..., ceil(n/block_rows),
+    ceil(k/128)]): E4M3 with one scale per block_rows x 128 block, block_rows 1 (activations) or 128 (weights)."""
+    _need(w, torch.bfloat16, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [n, k] or [e, n, k]")
+    if block_rows not in (1, _FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {_FP8_BLOCK}, got {block_rows}")
+    lead, (n, k) = tuple(w.shape[:-2]), w.shape[-2:]
+    _fp8_k(k)
+    codes, scales = _fp8_outputs(lead, n, k, block_rows, w.device)
+    _call(lib().nvfp4_fp8_quantize, "nvfp4_fp8_quantize", w.device, w.data_ptr(), lead[0] if lead else 1, n, k,
+          block_rows, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                residual_out: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """h = BF16(x + residual); RMS norm of h times weight -> (codes uint8 [m, k], scales float32 [m, ceil(k/128)], h).
+
+    x BF16 [m, k], weight BF16 [k].  With a residual (BF16 [m, k]) h is written to residual_out, which may be the
+    residual itself and is allocated when it is not given; without one h is None and x is normalized."""
+    _need(x, torch.bfloat16, "x")
+    _need(weight, torch.bfloat16, "weight")
+    if x.dim() != 2 or weight.shape != x.shape[1:]:
+        raise ValueError("x must be [m, k] and weight [k]")
+    m, k = x.shape
+    _fp8_k(k)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    else:
+        _need(residual, torch.bfloat16, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        else:
+            _need(residual_out, torch.bfloat16, "residual_out")
+        if residual.shape != x.shape or residual_out.shape != x.shape:
+            raise ValueError("residual and residual_out must have x's shape")
+    device = _one_device(x, weight, residual, residual_out)
+    codes, scales = _fp8_outputs((), m, k, 1, device)
+    _call(lib().nvfp4_rmsnorm_fp8, "nvfp4_rmsnorm_fp8", device, x.data_ptr(),
+          None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, m, k,
+          None if residual is None else residual_out.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, residual_out
+
+
+def silu_mul_fp8(gate_up: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """BF16 [m, 2n] (gate columns, then up columns) -> silu(gate) * up as (codes uint8 [m, n], scales float32
+    [m, ceil(n/128)])."""
+    _need(gate_up, torch.bfloat16, "gate_up")
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2 != 0:
+        raise ValueError("gate_up must be [m, 2n]")
+    m, n = gate_up.shape[0], gate_up.shape[1] // 2
+    _fp8_k(n)
+    codes, scales = _fp8_outputs((), m, n, 1, gate_up.device)
+    _call(lib().nvfp4_silu_mul_fp8, "nvfp4_silu_mul_fp8", gate_up.device, gate_up.data_ptr(), m, n, codes.data_ptr(),
+          scales.data_ptr())
+    return codes, scales
+
+
+def fp8_linear_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Workspace bytes nvfp4_fp8_linear can use for this shape (0: none)."""
+    b = lib().nvfp4_fp8_linear_workspace_bytes(m, n, k)
+    if b < 0:
+        raise ValueError(f"invalid linear shape m={m} n={n} k={k}")
+    return b
+
+
+def fp8_linear(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+               out: Optional[torch.Tensor] = None, workspace: Union[str, None, torch.Tensor] = "auto") -> torch.Tensor:
+    """Y[m, n] BF16 = X . W^T from E4M3 operands: xq [m, k] with scales xs [m, ceil(k/128)], wq [n, k] with scales
+    ws [ceil(n/128), ceil(k/128)].
+
+    workspace: "auto" allocates what the shape can use, None runs without a K split, a uint8 device tensor is
+    passed through (any contents)."""
+    _need_codes(xq, "xq")
+    _need(xs, torch.float32, "xs")
+    _need_codes(wq, "wq")
+    _need(ws, torch.float32, "ws")
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError("xq must be [m, k] and wq [n, k]")
+    (m, k), n = xq.shape, wq.shape[0]
+    _fp8_k(k)
+    kb = _fp8_blocks(k)
+    if xs.shape != (m, kb) or ws.shape != (_fp8_blocks(n), kb):
+        raise ValueError("xs must be [m, ceil(k/128)] and ws [ceil(n/128), ceil(k/128)]")
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != (m, n):
+            raise ValueError("out must be [m, n]")
+    if isinstance(workspace, torch.Tensor):
+        _need(workspace, torch.uint8, "workspace")
+    elif workspace is not None and workspace != "auto":
+        raise ValueError("workspace must be 'auto', None or a uint8 device tensor")
+    else:
+        need = fp8_linear_workspace_bytes(m, n, k) if workspace == "auto" else 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=xq.device) if need > 0 else None
+    device = _one_device(xq, xs, wq, ws, out, workspace)
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+    wptr, wbytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
+    _call(lib().nvfp4_fp8_linear, "nvfp4_fp8_linear", device, xq.data_ptr(), xs.data_ptr(), m, n, k, wq.data_ptr(),
+          ws.data_ptr(), out.data_ptr(), wptr, wbytes)
+    return out
+
+
+def fp8_linear_grouped_workspace_bytes(t: int, topk: int, e: int) -> int:
+    """Workspace bytes nvfp4_fp8_linear_grouped needs for t tokens, top-k routing over e experts."""
+    b = lib().nvfp4_fp8_linear_grouped_workspace_bytes(t, topk, e)
+    if b < 0:
+        raise ValueError(f"invalid grouped shape t={t} topk={topk} e={e}")
+    return b
+
+
+def fp8_linear_grouped(xq: torch.Tensor, xs: torch.Tensor, route: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t, j, :] = X[t, :] . W[route[t, j]]^T in BF16 from E4M3 operands: xq [t, k] with scales xs [t, ceil(k/128)],
+    an expert stack wq [e, n, k] with scales ws [e, ceil(n/128), ceil(k/128)], route int32 [t, topk].
+
+    Expert ids outside [0, e) give zero rows.  workspace: a uint8 device tensor of at least
+    fp8_linear_grouped_workspace_bytes(t, topk, e) bytes; allocated when it is not given."""
+    _need_codes(xq, "xq")
+    _need(xs, torch.float32, "xs")
+    _need(route, torch.int32, "route")
+    _need_codes(wq, "wq")
+    _need(ws, torch.float32, "ws")
+    if xq.dim() != 2 or wq.dim() != 3 or xq.shape[1] != wq.shape[2]:
+        raise ValueError("xq must be [t, k] and wq [e, n, k]")
+    (t, k), (e, n) = xq.shape, wq.shape[:2]
+    _fp8_k(k)
+    kb = _fp8_blocks(k)
+    if xs.shape != (t, kb) or ws.shape != (e, _fp8_blocks(n), kb):
+        raise ValueError("xs must be [t, ceil(k/128)] and ws [e, ceil(n/128), ceil(k/128)]")
+    if route.dim() != 2 or route.shape[0] != t:
+        raise ValueError("route must be [t, topk]")
+    topk = route.shape[1]
+    need = fp8_linear_grouped_workspace_bytes(t, topk, e)
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != (t, topk, n):
+            raise ValueError("out must be [t, topk, n]")
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    device = _one_device(xq, xs, route, wq, ws, out, workspace)
+    if out is None:
+        out = torch.empty((t, topk, n), dtype=torch.bfloat16, device=device)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(lib().nvfp4_fp8_linear_grouped, "nvfp4_fp8_linear_grouped", device, xq.data_ptr(), xs.data_ptr(), t, topk,
+          route.data_ptr(), e, n, k, wq.data_ptr(), ws.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
     return out

@@ -162,17 +162,21 @@ int64_t grouped_workspace_bytes(int64_t pairs, int64_t experts) {
   return ((3 * experts + 2 + pairs) * 4 + 15) / 16 * 16;
 }
 
-void launch_linear_grouped(const uint16_t* x, int64_t t_count, int64_t topk, const int32_t* route, int64_t experts,
-                           int64_t n, int64_t k, const uint8_t* packed, const uint8_t* scales, const float* tscale,
-                           uint16_t* y, void* workspace, hipStream_t s) {
-  const int64_t pairs = t_count * topk;
-  int32_t* ws = static_cast<int32_t*>(workspace);
+void launch_group_sort(const int32_t* route, int64_t pairs, int64_t experts, int32_t* ws, hipStream_t s) {
   if (experts <= kSortPermExperts && pairs <= kSortPermPairs)
     grp_sort_kernel<kSortPermExperts, kSortPermPairs><<<1, kSortThreads, 0, s>>>(route, pairs, experts, ws);
   else if (experts <= kSortLdsExperts)
     grp_sort_kernel<kSortLdsExperts, 0><<<1, kSortThreads, 0, s>>>(route, pairs, experts, ws);
   else
     grp_sort_kernel<0, 0><<<1, kSortThreads, 0, s>>>(route, pairs, experts, ws);
+}
+
+void launch_linear_grouped(const uint16_t* x, int64_t t_count, int64_t topk, const int32_t* route, int64_t experts,
+                           int64_t n, int64_t k, const uint8_t* packed, const uint8_t* scales, const float* tscale,
+                           uint16_t* y, void* workspace, hipStream_t s) {
+  const int64_t pairs = t_count * topk;
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  launch_group_sort(route, pairs, experts, ws, s);
   launch_prefill_grouped(x, topk, ws, pairs, experts, n, k, packed, scales, tscale, y, s);
 }
 

@@ -107,6 +107,9 @@ void launch_prefill_dma(const uint16_t* x, int64_t m, int64_t n, int64_t k, cons
 bool prefill_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k);
 int64_t prefill_grouped_tile_bound(int64_t pairs, int64_t experts);
 int64_t grouped_workspace_bytes(int64_t pairs, int64_t experts);
+// The sort alone: int32 cnt[experts] | pair_off[experts + 1] | tile_off[experts + 1] (128-row tiles) | perm[pairs],
+// the pairs with an id out of range last in perm.
+void launch_group_sort(const int32_t* route, int64_t pairs, int64_t experts, int32_t* ws, hipStream_t s);
 void launch_prefill_grouped(const uint16_t* x, int64_t topk, const int32_t* groups, int64_t pairs, int64_t experts,
                             int64_t n, int64_t k, const uint8_t* packed, const uint8_t* scales, const float* tscale,
                             uint16_t* y, hipStream_t s);
@@ -132,6 +135,28 @@ void launch_mx_dequant(const uint8_t* packed, const uint8_t* scales, int64_t row
 bool mx_gemm_supported(int64_t m, int64_t n, int64_t k);
 void launch_mx_gemm(const uint8_t* xq, const uint8_t* xs, int64_t m, const uint8_t* wq, const uint8_t* ws, int64_t n,
                     int64_t k, uint16_t* y, hipStream_t s);
+
+// E4M3 tensors with an FP32 scale per 1 x 128 (rows) or 128 x 128 (tiles) block; k a multiple of 16, the last block of
+// an axis may be short.  At most 2^31 - 1 blocks along k, 2^35 tiles and 2^35 rows of the norm.
+void launch_fp8_quantize_rows(const uint16_t* x, int64_t rows, int64_t k, uint8_t* codes, float* scales,
+                              hipStream_t s);
+void launch_fp8_quantize_tiles(const uint16_t* w, int64_t count, int64_t n, int64_t k, uint8_t* codes, float* scales,
+                               hipStream_t s);
+// silu(gate) * up of [rows, 2 n] -> [rows, n] (row blocks).
+void launch_silu_mul_fp8(const uint16_t* gate_up, int64_t rows, int64_t n, uint8_t* codes, float* scales,
+                         hipStream_t s);
+// RMS norm of BF16(x + residual) (residual and residual_out both NULL: of x).
+void launch_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, int64_t rows,
+                        int64_t k, uint16_t* residual_out, uint8_t* codes, float* scales, hipStream_t s);
+// E4M3 x E4M3 linear, and over an expert stack (workspace: grouped_workspace_bytes).
+bool fp8_linear_supported(int64_t m, int64_t n, int64_t k);
+int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
+                       const float* ws, uint16_t* y, void* workspace, hipStream_t s);
+bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k);
+void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_count, int64_t topk, const int32_t* route,
+                               int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
+                               void* workspace, hipStream_t s);
 
 // Plain streaming read of `bytes` bytes (a multiple of 16) of device memory by
 // stream_read_blocks(bytes) <= kStreamSinkWords workgroups; workgroup b stores the

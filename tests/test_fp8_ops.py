@@ -1,0 +1,423 @@
+"""The E4M3 operators with block scales: refusals of the C entry points and the binding (CPU), and the HIP kernels
+against the float64 oracle (GPU)."""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_weight_only_amd import binding as B
+from nvfp4_weight_only_amd import build as BUILD
+from nvfp4_weight_only_amd import workloads as WL
+from oracle import fp8_oracle as F
+
+U = 2.0 ** -24      # half a step of FP32, relative
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(B.lib_path()):
+        BUILD.build()
+    return B.lib()
+
+
+@pytest.fixture(scope="module")
+def nv():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import nvfp4_weight_only_amd as nv
+    nv.lib()
+    return nv
+
+
+# ---------------------------------------------------------------------------
+# CPU: the oracle's encoder, and what the entry points refuse.
+# ---------------------------------------------------------------------------
+def test_fp8_oracle_encoder_matches_torch():
+    grid = F._GRID
+    q = np.concatenate([grid, F._MID, F._MID * (1 + 2.0 ** -20), F._MID * (1 - 2.0 ** -20),
+                        np.random.default_rng(0).uniform(-448, 448, 4096)])
+    q = np.concatenate([q, -q])
+    want = torch.from_numpy(q.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(F.encode(q.astype(np.float32).astype(np.float64)), want)
+
+
+# Fake, never-dereferenced device addresses: validation fails before any HIP call.
+A, C, D, E, G, H, W = (i * 0x10000000 for i in range(1, 8))
+BIG = 2 ** 62
+
+
+def test_fp8_quantize_validation(L):
+    q = L.nvfp4_fp8_quantize
+    assert q(A, 1, 4, 128, 2, C, D, None) == B.ERR_UNSUPPORTED          # neither 1 nor 128 rows
+    assert q(A, 1, 4, 120, 1, C, D, None) == B.ERR_SHAPE                # k % 16 != 0
+    assert q(A, 1, 4, 0, 1, C, D, None) == B.ERR_SHAPE
+    assert q(A, -1, 4, 128, 1, C, D, None) == B.ERR_SHAPE and q(A, 1, -1, 128, 1, C, D, None) == B.ERR_SHAPE
+    assert q(A, 1, BIG, 128, 1, C, D, None) == B.ERR_SHAPE
+    assert q(A, 2 ** 20, 2 ** 20, 16, 1, C, D, None) == B.ERR_UNSUPPORTED
+    assert q(None, 0, 4, 128, 1, None, None, None) == B.OK and q(None, 1, 0, 128, 128, None, None, None) == B.OK
+    assert q(None, 1, 4, 128, 1, C, D, None) == B.ERR_NULL and q(A, 1, 4, 128, 1, C, None, None) == B.ERR_NULL
+    assert q(A + 8, 1, 4, 128, 1, C, D, None) == B.ERR_ALIGN and q(A, 1, 4, 128, 1, C, D + 4, None) == B.ERR_ALIGN
+    assert q(A, 1, 4, 128, 1, A + 512, D, None) == B.ERR_ALIAS          # codes overlap w
+    assert q(A, 1, 4, 128, 1, C, C + 256, None) == B.ERR_ALIAS          # scales overlap codes
+
+
+def test_rmsnorm_fp8_validation(L):
+    f = L.nvfp4_rmsnorm_fp8
+    assert f(A, None, C, EPS, 4, 100, None, D, E, None) == B.ERR_SHAPE
+    assert f(A, None, C, EPS, -1, 128, None, D, E, None) == B.ERR_SHAPE
+    for eps in (0.0, -1.0, float("nan"), float("inf"), 1e-39):
+        assert f(A, None, C, eps, 4, 128, None, D, E, None) == B.ERR_UNSUPPORTED
+    assert f(None, None, None, EPS, 0, 128, None, None, None, None) == B.OK
+    assert f(A, None, None, EPS, 4, 128, None, D, E, None) == B.ERR_NULL
+    assert f(A, G, C, EPS, 4, 128, None, D, E, None) == B.ERR_NULL       # residual without its output
+    assert f(A, None, C, EPS, 4, 128, G, D, E, None) == B.ERR_NULL       # and the reverse
+    assert f(A, G, C + 2, EPS, 4, 128, H, D, E, None) == B.ERR_ALIGN
+    assert f(A, G, C, EPS, 4, 128, G + 16, D, E, None) == B.ERR_ALIAS    # the residual's buffer, but shifted
+    assert f(A, G, C, EPS, 4, 128, A, D, E, None) == B.ERR_ALIAS         # over x
+    assert f(A, G, C, EPS, 4, 128, H, H, E, None) == B.ERR_ALIAS         # two outputs
+    assert f(A, G, C, EPS, 4, 128, G, G, E, None) == B.ERR_ALIAS         # in place, codes over the residual
+
+
+def test_silu_mul_fp8_validation(L):
+    f = L.nvfp4_silu_mul_fp8
+    assert f(A, 4, 24, C, D, None) == B.ERR_SHAPE and f(A, 4, 0, C, D, None) == B.ERR_SHAPE
+    assert f(None, 0, 128, None, None, None) == B.OK
+    assert f(None, 4, 128, C, D, None) == B.ERR_NULL
+    assert f(A, 4, 128, C + 8, D, None) == B.ERR_ALIGN
+    assert f(A, 4, 128, A + 4 * 512 - 16, D, None) == B.ERR_ALIAS        # codes over the last up columns
+
+
+def test_fp8_linear_validation(L):
+    f, wb = L.nvfp4_fp8_linear, L.nvfp4_fp8_linear_workspace_bytes
+    assert f(A, C, 4, 64, 24, D, E, G, None, 0, None) == B.ERR_SHAPE     # k % 16 != 0
+    assert f(A, C, 4, 0, 128, D, E, G, None, 0, None) == B.ERR_SHAPE
+    assert f(A, C, -1, 64, 128, D, E, G, None, 0, None) == B.ERR_SHAPE
+    assert f(A, C, 4, BIG, 128, D, E, G, None, 0, None) == B.ERR_SHAPE
+    assert f(A, C, 4, 64, 128, D, E, G, None, -1, None) == B.ERR_SHAPE
+    assert f(None, None, 0, 64, 128, D, E, None, None, 0, None) == B.OK  # m = 0
+    assert f(None, None, 0, 64, 128, None, E, None, None, 0, None) == B.ERR_NULL
+    assert f(A, None, 4, 64, 128, D, E, G, None, 0, None) == B.ERR_NULL
+    assert f(A, C + 4, 4, 64, 128, D, E, G, None, 0, None) == B.ERR_ALIGN
+    assert f(A, C, 4, 64, 128, D, E, G, W + 8, 1 << 20, None) == B.ERR_ALIGN
+    assert f(A, C, 4, 64, 128, D, E, A + 496, None, 0, None) == B.ERR_ALIAS
+    assert f(A, C, 4, 64, 128, D, E, D, None, 0, None) == B.ERR_ALIAS
+    assert wb(4, 64, 24) == -1 and wb(-1, 64, 128) == -1 and wb(4, 0, 128) == -1 and wb(0, 64, 128) == 0
+
+
+def test_fp8_linear_grouped_validation(L):
+    f, wb = L.nvfp4_fp8_linear_grouped, L.nvfp4_fp8_linear_grouped_workspace_bytes
+    need = wb(2, 2, 2)
+
+    def args(xq=A, t=2, topk=2, route=H, e=2, n=64, k=128, wq=D, y=G, ws=W, wsb=need):
+        return (xq, C, t, topk, route, e, n, k, wq, E, y, ws, wsb, None)
+    assert wb(-1, 1, 1) == -1 and wb(1, 0, 1) == -1 and wb(1, 1, 0) == -1 and wb(BIG, 4, 1) == -1
+    assert f(*args(topk=0)) == B.ERR_SHAPE and f(*args(e=0)) == B.ERR_SHAPE and f(*args(k=40)) == B.ERR_SHAPE
+    assert f(*args(n=0)) == B.ERR_SHAPE and f(*args(t=-1)) == B.ERR_SHAPE and f(*args(wsb=need - 16)) == B.ERR_SHAPE
+    assert f(*args(ws=None)) == B.ERR_NULL and f(*args(wq=None)) == B.ERR_NULL and f(*args(route=None)) == B.ERR_NULL
+    assert f(*args(route=H + 2)) == B.ERR_ALIGN and f(*args(ws=W + 8)) == B.ERR_ALIGN
+    assert f(*args(ws=H)) == B.ERR_ALIAS and f(*args(y=A)) == B.ERR_ALIAS and f(*args(ws=G)) == B.ERR_ALIAS
+    assert f(*args(xq=None, t=0, y=None, ws=None, wsb=0)) == B.OK
+
+
+# ---------------------------------------------------------------------------
+# GPU.
+# ---------------------------------------------------------------------------
+def bf16(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def f64(bits):
+    return WL.f32_from_bf16_bits(bits).astype(np.float64)
+
+
+def host(t):
+    return t.double().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+def same_scales(got, want):
+    return np.array_equal(host(got).view(np.uint32), np.where(np.isnan(want), np.float32("nan"), want)
+                          .astype(np.float32).view(np.uint32))
+
+
+def crafted():
+    """One row of 128: a tie on every E4M3 midpoint (amax 448 or a power of two times it), zeros, extremes."""
+    mids = np.concatenate([F._MID, [448.0, -448.0]])
+    rows = {"ties": mids, "ties, other signs": -mids, "zeros": np.zeros(16), "negative zeros": -np.zeros(16),
+            "huge": [3.0e38, -1e38, 1.0, -1e-30] * 4, "subnormal": [1e-40, -2e-39, 3e-41, 0.0] * 4,
+            "smallest": [9.2e-41, -9.2e-41] * 8, "infinity": [np.inf] + [1.0] * 15, "nan": [1.0] * 15 + [np.nan]}
+    out = {}
+    for name, v in rows.items():
+        r = np.zeros(-(-len(v) // 16) * 16, dtype=np.float32)
+        r[:len(v)] = v
+        out[name] = WL.bf16_bits_from_f32(r[None])
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,block_rows", [
+    ((1, 16), 1), ((1, 16), 128), ((3, 128), 1), ((8, 5120), 1), ((130, 272), 1), ((130, 272), 128), ((257, 144), 128),
+    ((1, 40000), 1), ((700, 8192), 1), ((3, 100, 208), 128), ((2, 128, 128), 128), ((3, 5, 208), 1)])
+def test_fp8_quantize_bit_exact(nv, shape, block_rows):
+    bits = WL.normal_bf16(shape, 0.02, 100 + shape[-1])
+    codes, scales = nv.fp8_quantize(bf16(bits), block_rows)
+    rc, rs = F.quantize(f64(bits), block_rows)
+    assert codes.shape == rc.shape and scales.shape == rs.shape
+    assert same_scales(scales, rs) and np.array_equal(host(codes), rc)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_fp8_quantize_crafted(nv, block_rows):
+    for name, bits in crafted().items():
+        codes, scales = nv.fp8_quantize(bf16(bits), block_rows)
+        rc, rs = F.quantize(f64(bits), block_rows)
+        assert same_scales(scales, rs), name
+        assert np.array_equal(host(codes), rc), name
+
+
+@pytest.mark.gpu
+def test_fp8_quantize_random_bits(nv):
+    """Every exponent: rows of random finite BF16 patterns against amax of every size."""
+    rng = np.random.default_rng(7)
+    bits = rng.integers(0, 1 << 16, size=(512, 256)).astype(np.uint16)
+    bits[(bits & 0x7F80) == 0x7F80] &= 0xBFFF
+    bits &= np.uint16(0x8000) | (np.linspace(0x100, 0x7F7F, 512).astype(np.uint16)[:, None])
+    codes, scales = nv.fp8_quantize(bf16(bits), 1)
+    rc, rs = F.quantize(f64(bits), 1)
+    assert same_scales(scales, rs) and np.array_equal(host(codes), rc)
+
+
+NORM_CASES = [(1, 16), (5, 128), (7, 400), (8, 5120), (300, 1024), (3, 8192), (3, 8208), (2, 32768), (2, 40016)]
+
+
+def norm_tolerance(k):
+    """Relative error of a scale: the sum of squares is a chain of at most 8 additions per piece and ceil(k / 8192)
+    or 4 pieces a thread, 6 in the wavefront and 16 across them (u each, halved by the root); the division by k, the
+    sum with eps, root and reciprocal and two more factors, u each."""
+    chain = 8 * max(4, -(-k // 8192)) + 22
+    return (chain / 2 + 6) * U * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k", NORM_CASES)
+@pytest.mark.parametrize("mode", ["plain", "residual", "in place"])
+def test_rmsnorm_fp8(nv, m, k, mode):
+    xb, rb = WL.normal_bf16((m, k), 1.0, 200 + k), WL.normal_bf16((m, k), 4.0, 201 + k)
+    gb = WL.normal_bf16((k,), 1.0, 202 + k)
+    x, g, r = bf16(xb), bf16(gb), bf16(rb)
+    h = f64(xb)
+    if mode == "plain":
+        codes, scales, h_out = nv.rmsnorm_fp8(x, g, EPS)
+        assert h_out is None
+    else:
+        hb = WL.bf16_bits_from_f32(WL.f32_from_bf16_bits(xb) + WL.f32_from_bf16_bits(rb))
+        h = f64(hb)
+        codes, scales, h_out = nv.rmsnorm_fp8(x, g, EPS, residual=r, residual_out=r if mode == "in place" else None)
+        assert np.array_equal(host(h_out), h)
+        assert mode == "in place" or np.array_equal(host(r), f64(rb))
+        assert (h_out.data_ptr() == r.data_ptr()) == (mode == "in place")
+    rc, rs = F.norm(h, f64(gb), EPS)
+    assert np.array_equal(host(codes), rc)
+    assert np.all(np.abs(host(scales) - rs) <= norm_tolerance(k) * rs)
+
+
+@pytest.mark.gpu
+def test_rmsnorm_fp8_odd_rows(nv):
+    """Zero rows and blocks, a row whose squares overflow FP32, infinities and NaN: only their own rows change."""
+    k = 384
+    xb = WL.normal_bf16((6, k), 1.0, 300)
+    xb[0] = 0
+    xb[1, 128:256] = 0
+    xb[2, 5] = WL.bf16_bits_from_f32(np.float32([3e38]))[0]
+    xb[3, 7] = 0x7F80
+    xb[4, 300] = 0x7FC0
+    g = np.ones(k, dtype=np.float32)
+    codes, scales, _ = nv.rmsnorm_fp8(bf16(xb), bf16(WL.bf16_bits_from_f32(g)), EPS)
+    codes, scales = host(codes), host(scales)
+    rc, rs = F.norm(f64(xb), g.astype(np.float64), EPS)
+    assert not codes[0].any() and not scales[0].any() and not codes[1, 128:256].any() and scales[1, 1] == 0
+    for row in (1, 5):
+        assert np.array_equal(codes[row], rc[row])
+        assert np.all(np.abs(scales[row] - rs[row]) <= norm_tolerance(k) * rs[row])
+    for row in (2, 3, 4):
+        assert np.all(codes[row] == 0x7F) and np.isnan(scales[row]).all()
+
+
+def silu_check(codes, scales, v):
+    """Codes and scales of v (float64) when v is computed in FP32 within delta: log2(e) g is carried in two floats and
+    the hardware's exp2 is within 1 ulp, so exp has about 4 u; the sum, division and product add u each, and the
+    quotient against an amax with the same error doubles that: 16 u is twice what they add up to."""
+    delta = 16 * U
+    amax = F.block_amax(v, 1)
+    assert np.all(np.abs(scales - amax / 448) <= delta * amax / 448 + 2.0 ** -149)
+    q = np.abs(F.quotients(v, 1))
+    got = F.values(codes)
+    step = np.exp2(np.floor(np.log2(np.maximum(q, 2.0 ** -6))) - 3)
+    assert np.all(np.abs(np.abs(got) - q) <= step / 2 + delta * q)
+    assert np.all((got == 0) | (np.sign(got) == np.sign(v)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(1, 16), (5, 128), (7, 400), (8, 17408), (600, 8192), (3, 20000)])
+def test_silu_mul_fp8(nv, m, n):
+    b = WL.normal_bf16((m, 2 * n), 3.0, 400 + n)
+    codes, scales = nv.silu_mul_fp8(bf16(b))
+    silu_check(host(codes), host(scales), F.silu_mul(f64(b[:, :n]), f64(b[:, n:])))
+
+
+@pytest.mark.gpu
+def test_silu_mul_fp8_extremes(nv):
+    """Gates from -3e38 to 3e38, with blocks apart so that small values keep their own scale; not finite blocks."""
+    gates = np.float32([-3e38, -200, -104, -90, -87, -60, -20, -1, -1e-3, -1e-30, 0, 1e-30, 1e-3, 1, 20, 87, 90, 3e38])
+    b = np.zeros((gates.size, 2 * 128), dtype=np.float32)
+    b[:, :128] = gates[:, None] * np.linspace(0.5, 1, 128)[None]
+    b[:, 128:] = np.where(np.abs(gates)[:, None] > 1e6, 0.25, 1.5)
+    bits = WL.bf16_bits_from_f32(b)
+    codes, scales = nv.silu_mul_fp8(bf16(bits))
+    v = F.silu_mul(f64(bits[:, :128]), f64(bits[:, 128:]))
+    keep = np.abs(v).max(axis=1) == 0
+    keep |= np.abs(v).max(axis=1) > 2.0 ** -120       # results below FP32's normal range lose their last bits
+    silu_check(host(codes)[keep], host(scales)[keep], v[keep])
+    for bad in (np.inf, -np.inf, np.nan):
+        for col in (3, 128 + 3):
+            c = b[13:15].copy()
+            c[0, col] = bad
+            codes, scales = nv.silu_mul_fp8(bf16(WL.bf16_bits_from_f32(c)))
+            assert np.all(host(codes)[0] == 0x7F) and np.isnan(host(scales)[0]).all()
+            assert np.isfinite(host(scales)[1]).all()
+
+
+def operands(m, n, k, seed, e=None):
+    """Random operands with uneven scales, as host arrays."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k)) * np.exp(rng.uniform(-2, 2, (m, 1)))
+    lead = () if e is None else (e,)
+    w = rng.standard_normal(lead + (n, k)) * 0.02 * np.exp(rng.uniform(-1, 1, lead + (n, 1)))
+    return (*F.quantize(x, 1), *F.quantize(w, 128))
+
+
+def exact_operands(m, n, k, seed, e=None):
+    """Operands whose products and sums are exact: codes of 0 and of magnitudes 0.5 .. 3.75 (products of at least
+    2^-2 with bits down to 2^-8, none dropped next to one below 2^4), scales 1 and 2.  The sums are multiples of 2^-8,
+    and exact in FP32 while their magnitudes stay below 2^16 (checked on sum |x w|, which bounds every
+    partial sum in any order).  The output is then the BF16 nearest to the exact sum."""
+    rng = np.random.default_rng(seed)
+    lead = () if e is None else (e,)
+
+    def codes(shape):
+        c = rng.integers(0x30, 0x48, size=shape).astype(np.uint8)      # 0.5 .. 3.75
+        return np.where(rng.random(shape) < 0.1, 0, c | (rng.integers(0, 2, size=shape) << 7)).astype(np.uint8)
+
+    def scales(shape):
+        return np.exp2(rng.integers(0, 2, size=shape)).astype(np.float32)
+    return (codes((m, k)), scales((m, -(-k // 128))), codes(lead + (n, k)),
+            scales(lead + (-(-n // 128), -(-k // 128))))
+
+
+def check_exact(y, ref, bound):
+    assert bound.max() < 2.0 ** 16
+    want = torch.from_numpy(ref).float().bfloat16().double().numpy()   # exact in FP32, one rounding
+    bad = host(y) != want
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} outputs differ, first {np.argwhere(bad)[:3].tolist()}"
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def check(y, ref, bound, k):
+    bad = ~(np.abs(host(y) - ref) <= F.linear_tolerance(ref, bound, k))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} outputs out of tolerance, first {np.argwhere(bad)[:3].tolist()}"
+
+
+LINEAR_CASES = [(1, 1, 16), (1, 16, 128), (1, 300, 1040), (2, 17, 144), (5, 64, 2048), (15, 130, 400), (16, 128, 512),
+                (17, 256, 640), (32, 1000, 1040), (33, 272, 256), (64, 512, 1024), (65, 129, 272), (100, 513, 384),
+                (128, 256, 2064), (200, 700, 1936), (256, 256, 128), (257, 300, 4112), (300, 130, 8192),
+                (513, 1030, 272), (700, 259, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", LINEAR_CASES)
+def test_fp8_linear(nv, m, n, k):
+    xq, xs, wq, ws = operands(m, n, k, 500 + m + n + k)
+    d = [dev(a) for a in (xq, xs, wq, ws)]
+    y = nv.fp8_linear(*d)
+    ref, bound = F.linear(xq, xs, wq, ws)
+    check(y, ref, bound, k)
+    check(nv.fp8_linear(*d, workspace=None), ref, bound, k)
+    ex = exact_operands(m, n, k, 501 + m + n + k)
+    check_exact(nv.fp8_linear(*(dev(a) for a in ex)), *F.linear(*ex))
+    assert torch.equal(nv.fp8_linear(*d), y)                       # the same bits again
+    big = torch.full((m + 2, n), 7.0, dtype=torch.bfloat16, device="cuda")   # rows around the output stay
+    if n % 8 == 0:
+        assert torch.equal(nv.fp8_linear(*d, out=big[1:m + 1]), y)
+        assert bool((big[0] == 7).all()) and bool((big[m + 1] == 7).all())
+
+
+@pytest.mark.gpu
+def test_fp8_linear_takes_float8_tensors(nv):
+    xq, xs, wq, ws = (dev(a) for a in operands(3, 40, 144, 600))
+    y = nv.fp8_linear(xq.view(torch.float8_e4m3fn), xs, wq.view(torch.float8_e4m3fn), ws)
+    assert torch.equal(y, nv.fp8_linear(xq, xs, wq, ws))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_fp8_linear_nan_and_zero(nv, m):
+    """A NaN code reaches its row or column only, also from the last, short block; zero scales give zeros."""
+    n, k = 200, 400
+    xq, xs, wq, ws = operands(m, n, k, 700)
+    xq[1, k - 1] = 0x7F
+    wq[150, 3] = 0xFF
+    xs[2] = 0
+    y = host(nv.fp8_linear(dev(xq), dev(xs), dev(wq), dev(ws)))
+    nan = np.zeros((m, n), dtype=bool)
+    nan[1], nan[:, 150] = True, True
+    assert np.array_equal(np.isnan(y), nan)
+    assert not y[2, np.arange(n) != 150].any()
+    clean = operands(m, n, k, 700)
+    ref, bound = F.linear(*clean)
+    ok = ~nan
+    ok[2] = False
+    assert np.all(np.abs(y - ref)[ok] <= F.linear_tolerance(ref, bound, k)[ok])
+
+
+def routing(kind, t, topk, e, seed):
+    rng = np.random.default_rng(seed)
+    if kind == "uniform":
+        r = rng.integers(0, e, size=(t, topk))
+    elif kind == "skew":
+        r = np.minimum(rng.geometric(0.5, size=(t, topk)) - 1, e - 1)
+    elif kind == "one":
+        r = np.full((t, topk), e - 1)
+    else:
+        r = np.full((t, topk), -1)
+    r = r.astype(np.int32)
+    if r.size >= 6 and kind != "none":
+        r.flat[2], r.flat[3], r.flat[5] = -1, e, 2 ** 31 - 1
+    return r
+
+
+GROUPED_CASES = [(1, 1, 1, 16, 128, "uniform"), (1, 8, 128, 64, 256, "uniform"), (4, 8, 16, 130, 400, "uniform"),
+                 (3, 2, 5, 33, 1040, "none"), (20, 4, 6, 300, 272, "skew"), (130, 2, 3, 64, 512, "one"),
+                 (200, 8, 16, 545, 256, "skew"), (300, 4, 6, 300, 1040, "uniform"), (40, 3, 700, 24, 144, "uniform"),
+                 (4200, 8, 4, 16, 128, "uniform")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,topk,e,n,k,kind", GROUPED_CASES)
+def test_fp8_linear_grouped(nv, t, topk, e, n, k, kind):
+    xq, xs, wq, ws = operands(t, n, k, 800 + t + n + k, e)
+    route = routing(kind, t, topk, e, 801)
+    d = [dev(a) for a in (xq, xs, route, wq, ws)]
+    y = nv.fp8_linear_grouped(*d)
+    ref, bound = F.linear_routed(xq, xs, route, wq, ws)
+    check(y, ref, bound, k)
+    assert not host(y)[(route < 0) | (route >= e)].any()
+    ex = exact_operands(t, n, k, 802 + t + n + k, e)
+    check_exact(nv.fp8_linear_grouped(dev(ex[0]), dev(ex[1]), d[2], dev(ex[2]), dev(ex[3])),
+                *F.linear_routed(ex[0], ex[1], route, ex[2], ex[3]))
+    dirty = torch.full((nv.fp8_linear_grouped_workspace_bytes(t, topk, e),), 0xAB, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(y, 3.0)
+    assert torch.equal(nv.fp8_linear_grouped(*d, out=out, workspace=dirty), y)
