@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libnvfp4.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["nvfp4_abi.hip", "quant_kernels.hip", "gemv.hip", "gemm.hip", "skinny.hip", "small_m.hip", "prefill.hip", "grouped.hip", "kv_gather.hip", "mxfp4.hip", "stream.hip",
-           "fp8_abi.hip", "fp8_quant.hip", "fp8_linear.hip"]
+           "fp8_abi.hip", "fp8_quant.hip", "fp8_linear.hip", "fp8_gemm.hip"]
 
 
 def hipcc() -> str:

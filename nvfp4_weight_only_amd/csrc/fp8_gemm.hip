@@ -1,0 +1,520 @@
+// E4M3 x E4M3 GEMM with FP32 scales per 128 elements of K, for many rows of X
+// (the arithmetic is fp8_linear.hip's).
+//
+// A workgroup of eight wavefronts owns a TN x TM tile of outputs (TN rows of W,
+// TM rows of X).  K advances in chunks of 128, one scale block each: both
+// operands' chunk goes to LDS by direct loads (16 bytes per lane, whole
+// 128-byte lines per row) into a ring of ST stages, so that up to ST - 1 chunks
+// are in flight behind the one in use.  Per chunk a wavefront holds its rows of
+// X in registers, passes over its rows of W 32 at a time, and each 32 x 32
+// block of outputs takes two 32x32x64 matrix instructions (the first with C =
+// 0) and 16 fused multiply-adds that scale the block's sum into the FP32
+// accumulators.  The multiply-adds of one block are issued behind the next
+// block's matrix instructions, which run meanwhile.
+//
+// LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
+// piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
+// covers all banks.
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace nvfp4 {
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) const void lds_t;
+
+constexpr int kChunk = 128;
+// How many chunks ahead of the loads to LDS lines are brought into L2.
+constexpr int kAhead = 2;
+
+struct GemmArgs {
+  const uint8_t* xq;
+  const float* xs;
+  const uint8_t* wq;
+  const float* ws;
+  uint16_t* y;
+  int64_t m, n, k;  // m: rows of y
+  int64_t ld;       // values from one row of y to the next
+  int kb, nb;
+  int n_tiles, m_tiles;
+  // Split: slices of K, and their FP32 sums [slices, m, n] (slices = 1: none).
+  int slices;
+  float* part;
+  // Grouped form: the sort's int32 arrays, pairs per token.
+  const int32_t* groups;
+  int64_t experts, topk;
+};
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(lds_t*)p; }
+
+// A pointer that is the same in every lane, in scalar registers.
+template <typename U>
+__device__ __forceinline__ const U* uniform(const U* p) {
+  const uint64_t b = (uint64_t)(uintptr_t)p;
+  return reinterpret_cast<const U*>(
+      ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
+      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b));
+}
+
+// A direct load to LDS from a uniform base: lane l's 16 bytes at offset off go
+// to lds + 16 l.  The asm block holds the wait states that the hardware leaves
+// to software on this path and that the compiler does not add around asm: five
+// between a vector instruction's write of a scalar register (the base may come
+// from a readfirstlane) and a memory instruction that reads it, one between a
+// write of M0 and a load to LDS.  No register result; the K loop waits for the
+// loads by count.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %2, %1" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
+               "s"(uniform(static_cast<const uint8_t*>(base))), "v"(off)
+               : "memory", "m0");
+}
+// The same for one load of 4 bytes per lane, to lds + 4 l.
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %2, %1" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
+               "s"(uniform(static_cast<const uint8_t*>(base))), "v"(off)
+               : "memory", "m0");
+}
+
+// 4 bytes of each lane's own address.
+__device__ __forceinline__ void dma4_lane(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
+               "v"(p)
+               : "memory", "m0");
+}
+
+// At most N of this wavefront's loads still in flight, and its LDS reads done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N <= 63, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+}
+
+__device__ __forceinline__ i32x8_t frag(const uint4& a, const uint4& b) {
+  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+__device__ __forceinline__ f32x4_t mfma128(const i32x8_t& a, const i32x8_t& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
+  const bf16x2_t r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+template <int TN, int TM>
+struct Stage {
+  uint4 w[TN * 8];
+  uint4 x[TM * 8];
+  float sx[TM];  // the chunk's scale of each row of X
+  float sw[64];  // ... of the tile's blocks of 128 rows of W (the first 3 at most are used)
+};
+
+template <int TN, int TM, int WN, int WM, int ST, bool GROUPED>
+__global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
+  static_assert(WN * WM == 8 && TN % (32 * WN) == 0 && TM % (16 * WM) == 0 && TN % 64 == 0 && TM % 64 == 0, "tile");
+  constexpr int NT = TN / WN / 16, MT = TM / WM / 16, T = NT * MT;  // 16 x 16 blocks of a wavefront
+  static_assert(T % 4 == 0 && NT % 2 == 0 && MT >= 2 && 128 % (TN / WN) == 0, "register rings; one scale of W");
+  constexpr int LW = TN / 64, LX = TM / 64, NL = LW + LX + 2;  // loads per wavefront and chunk
+  constexpr int QJ = NL <= T ? 1 : 2;  // loads behind each matrix instruction
+  static_assert(NL <= QJ * T, "a chunk's loads are issued before the next barrier");
+  __shared__ Stage<TN, TM> stage[ST];
+  __shared__ uint32_t sink[64];
+  static_assert(sizeof(stage) >= sizeof(uint16_t) * TN * TM, "the epilogue's tile fits the stages");
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = w % WN, wm = w / WN;
+
+  // Workgroups go to the 8 XCDs round-robin by id; when the count allows,
+  // consecutive ids of one XCD take all m tiles of consecutive n tiles, so a
+  // tile's rows of W are fetched into that XCD's L2 once.
+  const int tiles = p.n_tiles * p.m_tiles;
+  int id = (int)blockIdx.x;
+  const int slice = id / tiles;
+  id -= slice * tiles;
+  if ((tiles & 7) == 0) id = (id & 7) * (tiles >> 3) + (id >> 3);
+  const int nt = id / p.m_tiles, mt = id % p.m_tiles;
+  const int64_t n0 = (int64_t)nt * TN;
+  const uint8_t* wq = p.wq;
+  const float* ws = p.ws;
+  int64_t m0 = (int64_t)mt * TM, rows = p.m - m0 < TM ? p.m - m0 : TM;
+  const int32_t* perm = nullptr;
+  if constexpr (GROUPED) {
+    const int32_t* pair_off = p.groups + p.experts;
+    const int32_t* tile_off = p.groups + 2 * p.experts + 1;
+    perm = p.groups + 3 * p.experts + 2;
+    const int used = tile_off[p.experts];
+    if (mt >= used) {  // zero rows for the pairs whose id is out of range
+      const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN;
+      for (int64_t i = (int64_t)pair_off[p.experts] + mt - used; i < p.m; i += p.m_tiles - used)
+        for (int64_t c = tid; c < cols; c += 512) p.y[perm[i] * p.ld + n0 + c] = 0;
+      return;
+    }
+    int64_t lo = 0, hi = p.experts - 1;  // the expert with tile_off[e] <= mt < tile_off[e + 1]
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (tile_off[mid] <= mt) lo = mid;
+      else hi = mid - 1;
+    }
+    m0 = pair_off[lo] + (int64_t)(mt - tile_off[lo]) * TM;
+    rows = pair_off[lo + 1] - m0 < TM ? pair_off[lo + 1] - m0 : TM;
+    wq += lo * p.n * p.k;
+    ws += lo * p.nb * p.kb;
+  }
+
+  // This wavefront's loads: instruction j fills rows 8 (w + 8 j) .. + 7, lane l
+  // row + l / 8, physical piece l % 8.  Rows past N or the tile's rows of X
+  // repeat the last one (their results are not stored).
+  const int lrow = lane >> 3, piece = (lane & 7) ^ lrow;  // row & 7 == lrow
+  const auto x_row = [&](int r) -> int64_t {              // the row of X behind row r of the tile
+    const int64_t rm = r < rows ? r : rows - 1;
+    return GROUPED ? (int64_t)((uint32_t)perm[m0 + rm] / (uint32_t)p.topk) : rm;
+  };
+  const uint8_t* wbase = uniform(wq + n0 * p.k);
+  const uint8_t* xbase = uniform(GROUPED ? p.xq : p.xq + m0 * p.k);
+  uint32_t offw[LW], offx[LX];
+#pragma unroll
+  for (int j = 0; j < LW; ++j) {
+    const int64_t r = 8 * (w + 8 * j) + lrow, rn = n0 + r < p.n ? r : p.n - 1 - n0;
+    offw[j] = (uint32_t)(rn * p.k + 16 * piece);
+  }
+#pragma unroll
+  for (int j = 0; j < LX; ++j) offx[j] = (uint32_t)(x_row(8 * (w + 8 * j) + lrow) * p.k + 16 * piece);
+  // Scales: wavefront w < LX the rows 64 w .. + 63 of X, the others the blocks of W.
+  const float* sbase;
+  uint32_t soff;
+  if (w < LX) {
+    sbase = GROUPED ? p.xs : p.xs + m0 * p.kb;
+    soff = (uint32_t)(4 * x_row(64 * w + lane) * p.kb);
+  } else {
+    const int64_t b0 = n0 / 128, b = b0 + lane < p.nb ? lane : p.nb - 1 - b0;
+    sbase = ws + b0 * p.kb;
+    soff = (uint32_t)(4 * b * p.kb);
+  }
+  sbase = uniform(sbase);
+
+  // Lines brought into L2 ahead of their chunk's loads (one 4-byte read each, to
+  // a part of LDS that nothing reads): the tiles that run on this XCD at the same
+  // time and share rows of W (m tiles, up to 8) or of X share this work.
+  const int share_w = p.m_tiles < 8 ? p.m_tiles : 8, share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
+  const int lines_w = (TN + share_w - 1) / share_w, lines_x = (TM + share_x - 1) / share_x;
+  const uint8_t* pf;
+  {
+    const int i = 8 * lane + w;
+    if (i < lines_w || i >= lines_w + lines_x) {
+      const int r = (i < lines_w ? i : 0) * share_w + mt % share_w;
+      pf = wbase + (n0 + r < p.n ? r : p.n - 1 - n0) * p.k;
+    } else {
+      const int r = (i - lines_w) * share_x + nt % share_x;
+      pf = xbase + x_row(r < TM ? r : TM - 1) * p.k;
+    }
+  }
+  // Chunks of this slice.
+  const int c0 = (int)((int64_t)p.kb * slice / p.slices), c1 = (int)((int64_t)p.kb * (slice + 1) / p.slices);
+  const int last = c1 - 1;
+  // A last, short chunk: pieces past the end of K are read from the row's last
+  // one, and X's are set to zero in LDS when they have landed (finish).  W's keep
+  // the copy: times zero, or NaN where that row's sum is NaN by its own piece.
+  const int ktail = (int)(p.k & (kChunk - 1));
+  const bool past = ktail != 0 && 16 * piece >= ktail;
+  const uint32_t back = past ? (uint32_t)(16 * piece - (ktail - 16)) : 0u;
+
+  // Load q (of NL) of chunk c into stage s; past the end the last chunk again, so
+  // that every chunk leaves the same number of loads behind.
+  const auto issue = [&](int q, int c, int s) {
+    const int cc = c < last ? c : last;
+    Stage<TN, TM>& sg = stage[s];
+    const int64_t k0 = (int64_t)cc * kChunk;
+    const uint32_t bk = cc == p.kb - 1 ? back : 0u;
+    if (q < LW) dma16(wbase + k0, offw[q < LW ? q : 0] - bk, lds_addr(&sg.w[0]) + 1024 * w + 8192 * q);
+    else if (q < LW + LX)
+      dma16(xbase + k0, offx[q >= LW && q < LW + LX ? q - LW : 0] - bk,
+            lds_addr(&sg.x[0]) + 1024 * w + 8192 * (q - LW));
+    else if (q == LW + LX)
+      dma4(sbase + cc, soff, w < LX ? lds_addr(&sg.sx[64 * (w < LX ? w : 0)]) : lds_addr(&sg.sw[0]));
+    else
+      dma4_lane(pf + (int64_t)(cc + kAhead < last ? cc + kAhead : last) * kChunk, lds_addr(&sink[0]));
+  };
+  // This wavefront's loads of chunk c, in stage s, have landed.
+  const auto finish = [&](int c, int s) {
+    if (ktail == 0 || c != p.kb - 1) return;
+    if (past) {
+#pragma unroll
+      for (int j = 0; j < LX; ++j) stage[s].x[64 * (w + 8 * j) + lane] = make_uint4(0, 0, 0, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  };
+
+  f32x4_t acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // Byte offsets in a stage of this lane's first row of each operand, at the
+  // lane group's first piece (2 g); the second piece is the offset ^ 16.
+  const uint32_t lane_off = (uint32_t)(128 * l16 + 16 * ((2 * g) ^ (l16 & 7)));
+  const uint32_t rx = lane_off + (uint32_t)(sizeof(uint4) * TN * 8) + 128 * 16 * wm * MT;
+  const uint32_t rw = lane_off + 128 * 16 * wn * NT;
+  const char* const lds0 = reinterpret_cast<const char*>(&stage[0]);
+  const auto read = [&](uint32_t off, int rows16) {
+    return frag(*reinterpret_cast<const uint4*>(lds0 + off + 2048 * rows16),
+                *reinterpret_cast<const uint4*>(lds0 + (off ^ 16) + 2048 * rows16));
+  };
+  const auto meet = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+
+  // The matrix instructions of a wavefront run on without a break from chunk to
+  // chunk: fragments of W are read one row of blocks ahead (two registers sets),
+  // and behind the last use of each fragment of X the next chunk's is read over
+  // it.  The one barrier of a chunk stands before its last row of blocks, where
+  // everything of this chunk's stage has been read and the next chunk has
+  // landed: after it the next chunk's fragments are read, and the chunk that
+  // takes this stage is loaded, one load behind each matrix instruction.
+#pragma unroll
+  for (int s = 0; s < ST; ++s)
+#pragma unroll
+    for (int q = 0; q < NL; ++q) issue(q, c0 + s, s);
+  wait_loads<(ST - 1) * NL>();
+  finish(c0, 0);
+  meet();
+  i32x8_t a[2], b[MT];
+  float sx[MT], sw;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    b[j] = read(rx, j);
+    sx[j] = stage[0].sx[16 * wm * MT + l16 + 16 * j];
+  }
+  a[0] = read(rw, 0);
+  sw = stage[0].sw[((int)(n0 & 127) + 16 * wn * NT) >> 7];
+  // Sums of the last blocks: block t is scaled behind the matrix instruction of
+  // block t + 2, so that the multiply-adds never wait for it.
+  f32x4_t d[4];
+  float f[MT], f_old[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < MT; ++j) f[j] = 0.0f;
+  int sidx = 0;
+  for (int c = c0; c < c1; ++c) {
+    const int here = sidx;
+    sidx = sidx + 1 == ST ? 0 : sidx + 1;
+    const uint32_t so = (uint32_t)(here * sizeof(Stage<TN, TM>)), sn = (uint32_t)(sidx * sizeof(Stage<TN, TM>));
+    f_old[0] = f[MT - 2], f_old[1] = f[MT - 1];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) f[j] = sx[j] * sw;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i < NT - 1) {
+        a[(i + 1) & 1] = read(so + rw, i + 1);
+      } else {
+        wait_loads<(ST - 2) * NL + 1>();
+        finish(c + 1, sidx);
+        meet();
+        a[0] = read(sn + rw, 0);
+        sw = stage[sidx].sw[((int)(n0 & 127) + 16 * wn * NT) >> 7];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        // In this order: the compiler would gather the matrix instructions and
+        // sink the multiply-adds.
+        const int t = i * MT + j, u = (t + T - 2) % T;
+        d[t & 3] = mfma128(a[i & 1], b[j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i == NT - 1) {
+          b[j] = read(sn + rx, j);
+          sx[j] = stage[sidx].sx[16 * wm * MT + l16 + 16 * j];
+#pragma unroll
+          for (int q = QJ * j; q < QJ * (j + 1) && q < NL; ++q) issue(q, c + ST, here);
+        } else {
+#pragma unroll
+          for (int q = QJ * (t + MT); q < QJ * (t + MT + 1) && q < NL; ++q)
+            issue(q, c - 1 + ST, here == 0 ? ST - 1 : here - 1);
+        }
+        const float fu = t < 2 ? f_old[t] : f[u % MT];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[u][e] = __builtin_fmaf(d[u & 3][e], fu, acc[u][e]);
+        asm volatile("" : "+v"(acc[u]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = T - 2; u < T; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[u][e] = __builtin_fmaf(d[u & 3][e], f[u % MT], acc[u][e]);
+  wait_loads<0>();  // the repeat loads past the end have landed
+  __syncthreads();
+
+  // Block t = i MT + j: lane (l16, g) holds row 16 j + l16 of X and rows 4 g +
+  // 0..3 of the 16 of W, four neighbouring outputs of one row.
+  const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN;
+  if (p.slices > 1) {  // FP32 sums of this slice; n is a multiple of 4 there
+    float* part = p.part + (int64_t)slice * p.m * p.n;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int r = 16 * (wm * MT + t % MT) + l16, col = 16 * (wn * NT + t / MT) + 4 * g;
+      if (r < rows && col < cols) *reinterpret_cast<f32x4_t*>(part + (m0 + r) * p.n + n0 + col) = acc[t];
+    }
+    return;
+  }
+  // The BF16 tile goes through LDS (the stages are free), so that the stores to
+  // Y are whole rows: [TM rows][TN columns], 16-byte pieces swizzled as above.
+  uint16_t* yt = reinterpret_cast<uint16_t*>(&stage[0]);
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int r = 16 * (wm * MT + t % MT) + l16, col = 16 * (wn * NT + t / MT) + 4 * g;
+    *reinterpret_cast<uint2*>(yt + r * TN + 8 * ((col >> 3) ^ (r & 7)) + (col & 4)) =
+        make_uint2(bf16x2_of(acc[t][0], acc[t][1]), bf16x2_of(acc[t][2], acc[t][3]));
+  }
+  __syncthreads();
+  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+  const bool vec = (p.n & 7) == 0 && (p.ld & 7) == 0;
+#pragma unroll 4
+  for (int pi = tid; pi < TM * (TN / 8); pi += 512) {
+    const int r = pi / (TN / 8), c8 = 8 * (pi - r * (TN / 8));
+    if (r >= rows || c8 >= cols) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(yt + r * TN + 8 * ((c8 >> 3) ^ (r & 7)));
+    const int64_t row = GROUPED ? (int64_t)perm[m0 + r] : m0 + r;
+    uint16_t* dst = p.y + row * p.ld + n0 + c8;
+    if (vec) {
+      *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{v.x, v.y, v.z, v.w};
+    } else {
+      const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (c8 + t < cols) dst[t] = (uint16_t)(e[t >> 1] >> (16 * (t & 1)));
+    }
+  }
+}
+
+// Sums of the slices in slice order, 4 outputs per thread.
+__global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__ part, int slices, int64_t quads,
+                                                       uint16_t* __restrict__ y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  f32x4_t s = reinterpret_cast<const f32x4_t*>(part)[i];
+  for (int t = 1; t < slices; ++t) {
+    const f32x4_t o = reinterpret_cast<const f32x4_t*>(part)[(int64_t)t * quads + i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += o[e];
+  }
+  reinterpret_cast<uint2*>(y)[i] = make_uint2(bf16x2_of(s[0], s[1]), bf16x2_of(s[2], s[3]));
+}
+
+}  // namespace
+
+namespace {
+
+// Tile shapes.  Measured per chunk of 128 and per tile (first loads and
+// epilogue), in ns, with a CU's slots filled: 256 x 256 at 1.9 PFLOP/s over the
+// chip, the smaller ones less (more LDS reads per product), but with finer
+// steps for sizes that leave CUs idle.
+struct Shape {
+  int tn, tm, per_cu;
+  double chunk, tile;
+};
+constexpr Shape kShapes[3] = {{256, 256, 1, 1900, 9000}, {256, 128, 1, 1150, 7000}, {128, 64, 2, 1150, 7000}};
+constexpr int kCus = 256;
+
+int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
+
+// Estimated ns of the tiles over the chip, each K slice `chunks` long.
+double shape_ns(const Shape& s, int64_t wgs, int64_t chunks) {
+  const int64_t slots = (int64_t)kCus * s.per_cu;
+  // Half-filled CUs: a workgroup alone on its CU takes a little under half the pair's time.
+  if (s.per_cu == 2 && wgs <= kCus) return s.tile + 480.0 * (double)chunks;
+  return (double)((wgs + slots - 1) / slots) * (s.tile + s.chunk * (double)chunks);
+}
+
+struct Plan {
+  int shape = 0, slices = 1;
+  int64_t n1 = 0;  // columns of the 256 x 256 tiles that come first (0: one launch)
+};
+
+// The cheapest of: one shape; one shape with K split (the slices' sums take a
+// write, a read and a second launch); whole rounds of 256 x 256 tiles and a
+// second launch with small tiles for the columns left over, which would
+// otherwise occupy a round by themselves.
+Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
+  const int64_t chunks = (k + kChunk - 1) / kChunk;
+  Plan best;
+  double cost = 1e300;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t tiles = tiles_of(kShapes[i], m, n);
+    for (int s = 1; s <= 8; ++s) {
+      if (s > 1 && (!split || (n & 3) != 0 || chunks < 4 * s || tiles * s > 2 * kCus ||
+                    m * n > ((int64_t)1 << 26) / s))
+        break;
+      const double ns = shape_ns(kShapes[i], tiles * s, (chunks + s - 1) / s) +
+                        (s > 1 ? 5000.0 + 8.0 * (double)(m * n) * s / 4000.0 : 0.0);
+      if (ns < cost) cost = ns, best = Plan{i, s, 0};
+    }
+  }
+  const int64_t m_tiles = (m + 255) / 256, n_tiles = (n + 255) / 256;
+  const int64_t rounds = n_tiles * m_tiles / kCus, cols = rounds * kCus / m_tiles;  // n tiles of whole rounds
+  if (rounds > 0 && cols > 0 && cols < n_tiles) {
+    const double ns = shape_ns(kShapes[0], cols * m_tiles, chunks) + 3000.0 +
+                      shape_ns(kShapes[2], tiles_of(kShapes[2], m, n - 256 * cols), chunks);
+    if (ns < cost) best = Plan{0, 1, 256 * cols};
+  }
+  return best;
+}
+
+template <int TN, int TM, int WN, int WM, int ST>
+void launch_tiles(GemmArgs a, hipStream_t s) {
+  a.n_tiles = (int)((a.n + TN - 1) / TN);
+  a.m_tiles = (int)((a.m + TM - 1) / TM);
+  fp8_gemm_kernel<TN, TM, WN, WM, ST, false>
+      <<<dim3((unsigned)((int64_t)a.n_tiles * a.m_tiles * a.slices)), 512, 0, s>>>(a);
+}
+
+void launch_shape(int shape, const GemmArgs& a, hipStream_t s) {
+  switch (shape) {
+    case 0: launch_tiles<256, 256, 2, 4, 2>(a, s); break;
+    case 1: launch_tiles<256, 128, 4, 2, 3>(a, s); break;
+    default: launch_tiles<128, 64, 4, 2, 3>(a, s); break;
+  }
+}
+
+}  // namespace
+
+// 32-bit offsets inside a tile, and at most 2^32 threads.
+bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) {
+  return k <= ((int64_t)1 << 23) && (m + 63) / 64 <= ((int64_t)1 << 22) / ((n + 127) / 128);
+}
+
+int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  const Plan p = gemm_plan(m, n, k, true);
+  return p.slices > 1 ? 4 * m * n * p.slices : 0;
+}
+
+void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
+                     const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
+  const Plan p = gemm_plan(m, n, k, workspace != nullptr);
+  GemmArgs a{xq, xs, wq, ws, y, m, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128), 0, 0, p.slices,
+             static_cast<float*>(workspace), nullptr, 1, 1};
+  if (p.n1 == 0) {
+    launch_shape(p.shape, a, s);
+  } else {
+    a.n = p.n1, a.nb = (int)(p.n1 / 128);
+    launch_shape(0, a, s);
+    a.wq = wq + p.n1 * k, a.ws = ws + p.n1 / 128 * a.kb, a.y = y + p.n1;
+    a.n = n - p.n1, a.nb = (int)((n - p.n1 + 127) / 128);
+    launch_shape(2, a, s);
+  }
+  if (p.slices > 1) {
+    const int64_t quads = m * n / 4;
+    fp8_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a.part, p.slices, quads, y);
+  }
+}
+
+}  // namespace nvfp4

@@ -151,7 +151,11 @@ bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
   return n <= ((int64_t)1 << 26) && (m + 63) / 64 <= 65535 && k <= ((int64_t)1 << 37);
 }
 
-int64_t fp8_linear_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+static bool use_gemm(int64_t m, int64_t n, int64_t k) { return m > 64 && fp8_gemm_supported(m, n, k); }
+
+int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
+}
 
 bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
   return fp8_linear_supported(1, n, k) && topk <= ((int64_t)1 << 30) / t_count &&
@@ -162,6 +166,7 @@ void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n,
                        const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
   const SkinnyArgs a{xq, xs, wq, ws, y, m, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), nullptr, 1, 1};
   const unsigned gx = (unsigned)((n + 15) / 16);
+  if (use_gemm(m, n, k)) return launch_fp8_gemm(xq, xs, m, n, k, wq, ws, y, workspace, s);
   if (m <= 16) fp8_skinny_kernel<1><<<dim3(gx, 1), 64 * kSkWaves, 0, s>>>(a);
   else fp8_skinny_kernel<4><<<dim3(gx, (unsigned)((m + 63) / 64)), 64 * kSkWaves, 0, s>>>(a);
 }

@@ -355,6 +355,28 @@ def test_fp8_linear(nv, m, n, k):
         assert bool((big[0] == 7).all()) and bool((big[m + 1] == 7).all())
 
 
+def decoded(codes, scales, block_rows):
+    r, k = codes.shape[-2:]
+    sp = scales.repeat_interleave(block_rows, -2)[..., :r, :].repeat_interleave(128, -1)[..., :k]
+    return codes.view(torch.float8_e4m3fn).float() * sp
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(2048, 17408, 640), (4100, 4500, 400), (333, 5000, 4112), (700, 9000, 1040),
+                                   (1500, 1030, 2048), (129, 3000, 3088), (8, 17408, 5120), (64, 5120, 4096),
+                                   (1, 34816, 5120), (31, 5120, 8208)])
+def test_fp8_linear_large_exact(nv, m, n, k):
+    """Sizes of every launch plan, with operands whose sums are exact in FP32: equal to torch's FP32 product."""
+    d = [dev(a) for a in exact_operands(m, n, k, 650 + m + n + k)]
+    x, w = decoded(d[0], d[1], 1), decoded(d[2], d[3], 128)
+    assert float((x.abs() @ w.abs().T).max()) < 2.0 ** 16
+    want = (x @ w.T).bfloat16()
+    for ws in ("auto", None):
+        y = nv.fp8_linear(*d, workspace=ws)
+        bad = y != want
+        assert not bool(bad.any()), f"workspace {ws}: {int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
+
+
 @pytest.mark.gpu
 def test_fp8_linear_takes_float8_tensors(nv):
     xq, xs, wq, ws = (dev(a) for a in operands(3, 40, 144, 600))
