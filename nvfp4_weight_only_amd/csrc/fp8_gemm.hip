@@ -422,7 +422,8 @@ struct Shape {
   int tn, tm, per_cu;
   double chunk, tile;
 };
-constexpr Shape kShapes[3] = {{256, 256, 1, 1900, 9000}, {256, 128, 1, 1150, 7000}, {128, 64, 2, 1150, 7000}};
+constexpr Shape kShapes[4] = {
+    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1150, 7000}, {128, 64, 2, 1150, 7000}, {256, 64, 1, 1200, 7000}};
 constexpr int kCus = 256;
 
 int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
@@ -448,7 +449,7 @@ Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
   const int64_t chunks = (k + kChunk - 1) / kChunk;
   Plan best;
   double cost = 1e300;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const int64_t tiles = tiles_of(kShapes[i], m, n);
     for (int s = 1; s <= 8; ++s) {
       if (s > 1 && (!split || (n & 3) != 0 || chunks < 4 * s || tiles * s > 2 * kCus ||
@@ -481,7 +482,8 @@ void launch_shape(int shape, const GemmArgs& a, hipStream_t s) {
   switch (shape) {
     case 0: launch_tiles<256, 256, 2, 4, 2>(a, s); break;
     case 1: launch_tiles<256, 128, 4, 2, 3>(a, s); break;
-    default: launch_tiles<128, 64, 4, 2, 3>(a, s); break;
+    case 2: launch_tiles<128, 64, 4, 2, 3>(a, s); break;
+    default: launch_tiles<256, 64, 8, 1, 3>(a, s); break;
   }
 }
 

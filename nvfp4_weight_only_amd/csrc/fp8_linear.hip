@@ -7,6 +7,8 @@
 // operand (columns m), so the four results of a lane belong to one activation
 // row: one factor xs[m, b] ws[n / 128, b] per lane.  Both operands place the
 // same element of K at the same position, whatever the order within the block.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -43,17 +45,25 @@ struct RowSpan {
   __device__ __forceinline__ int64_t x_row(int64_t i) const { return perm ? perm[first + i] / topk : first + i; }
 };
 
-constexpr int kSkWaves = 8;
+constexpr int kMaxWaves = 16;
 
-// 16 rows of W against 16 MT rows of X per workgroup; wavefront w takes blocks
-// w, w + 8, ... of K, and the eight partial sums meet in LDS, added in
-// wavefront order.
-template <int MT>
+// 16 NT rows of W against 16 MT rows of X by a workgroup of `waves` wavefronts,
+// each of which takes a contiguous share of the whole blocks of K, U blocks at a
+// time, with the next U blocks of W already on their way; the last wavefront
+// adds the last, short block.  Their sums meet in LDS and are added in wavefront
+// order.  SXL: the rows' scales are first copied to LDS.
+template <int MT, int NT, int U, bool SXL>
 __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* wq, const float* ws, int64_t n0,
-                                            const RowSpan& rows, int64_t i0, float (&red)[kSkWaves][MT][256]) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t wr = n0 + r < p.n ? n0 + r : p.n - 1;
-  const uint8_t* wp = wq + wr * p.k + 16 * g;
+                                            const RowSpan& rows, int64_t i0, int waves, f32x4_t* red, float* sxl) {
+  constexpr int T = MT * NT;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint8_t* wp[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t wr = n0 + 16 * t + r < p.n ? n0 + 16 * t + r : p.n - 1;
+    wp[t] = wq + wr * p.k + 16 * g;
+  }
   const float* wsp = ws + (n0 >> 7) * p.kb;
   const uint8_t* xp[MT];
   const float* xsp[MT];
@@ -64,62 +74,141 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
     xp[t] = p.xq + xr * p.k + 16 * g;
     xsp[t] = p.xs + xr * p.kb;
   }
-  f32x4_t acc[MT];
+  const int ld = p.kb | 1;  // an odd number of words from row to row
+  if constexpr (SXL) {
+    for (int i = threadIdx.x; i < 16 * MT * p.kb; i += blockDim.x) {
+      const int rr = i / p.kb, c = i - rr * p.kb;
+      const int64_t xi = i0 + rr < rows.count ? i0 + rr : rows.count - 1;
+      sxl[rr * ld + c] = p.xs[rows.x_row(xi) * p.kb + c];
+    }
+    __syncthreads();
+  }
+  const auto sx = [&](int t, int b) -> float { return SXL ? sxl[(16 * t + r) * ld + b] : xsp[t][b]; };
+  const auto load = [](const uint8_t* q) { return *reinterpret_cast<const uint4*>(q); };
+  f32x4_t acc[T];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b = w; b < p.kb; b += kSkWaves) {
-    const int64_t k0 = (int64_t)b * 128;
-    // Pieces past the end of a row are zero in both operands.
-    const bool in0 = k0 + 16 * g < p.k, in1 = k0 + 64 + 16 * g < p.k;
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    const uint4 a0 = in0 ? *reinterpret_cast<const uint4*>(wp + k0) : z;
-    const uint4 a1 = in1 ? *reinterpret_cast<const uint4*>(wp + k0 + 64) : z;
-    const float sw = wsp[b];
+  for (int t = 0; t < T; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int full = (int)(p.k >> 7);  // whole blocks
+  const int b0 = (int)((int64_t)full * w / waves), b1 = (int)((int64_t)full * (w + 1) / waves);
+
+  // Past the share's end: the last block again (with factor zero).
+  const auto load_w = [&](int b, uint4 (&a)[U][NT][2]) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint4 b0 = in0 ? *reinterpret_cast<const uint4*>(xp[t] + k0) : z;
-      const uint4 b1 = in1 ? *reinterpret_cast<const uint4*>(xp[t] + k0 + 64) : z;
-      const float s = xsp[t][b] * sw;
-      const f32x4_t d = mfma128(a0, a1, b0, b1);
+    for (int u = 0; u < U; ++u) {
+      const int64_t o = 128 * (int64_t)(b + u < b1 ? b + u : b1 - 1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], s, acc[t][e]);
+      for (int t = 0; t < NT; ++t) a[u][t][0] = load(wp[t] + o), a[u][t][1] = load(wp[t] + o + 64);
+    }
+  };
+  // Blocks b .. b + U with W in a.  X is loaded before the next blocks of W:
+  // loads return in order, and W's come from further away.
+  const auto step = [&](int b, const uint4 (&a)[U][NT][2], auto more, uint4 (&next)[U][NT][2]) {
+    uint4 x[U][MT][2];
+    float f[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int bb = b + u < b1 ? b + u : b1 - 1;
+      const int64_t o = 128 * (int64_t)bb;
+      const float sw = wsp[bb] * (b + u < b1 ? 1.0f : 0.0f);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        x[u][t][0] = load(xp[t] + o), x[u][t][1] = load(xp[t] + o + 64);
+        f[u][t] = sx(t, bb) * sw;
+      }
+    }
+    if constexpr (decltype(more)::value) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(b + U, next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const f32x4_t d = mfma128(a[u][t / MT][0], a[u][t / MT][1], x[u][t % MT][0], x[u][t % MT][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], f[u][t % MT], acc[t][e]);
+      }
+  };
+  if (b0 < b1) {
+    uint4 wa[U][NT][2], wb[U][NT][2];
+    load_w(b0, wa);
+    int b = b0;
+    for (; b + 2 * U < b1; b += 2 * U) {
+      step(b, wa, std::true_type(), wb);
+      step(b + U, wb, std::true_type(), wa);
+    }
+    if (b + U < b1) {
+      step(b, wa, std::true_type(), wb);
+      step(b + U, wb, std::false_type(), wa);
+    } else {
+      step(b, wa, std::false_type(), wb);
     }
   }
+  if (full < p.kb && w == waves - 1) {
+    // Pieces past the end of a row: the row's last piece of W, zeros of X.
+    const int64_t k0 = 128 * (int64_t)full, end = p.k - 16 - 16 * g;
+    const bool in0 = k0 <= end, in1 = k0 + 64 <= end;
+    const int64_t o0 = in0 ? k0 : end, o1 = in1 ? k0 + 64 : end;
+    const float sw = wsp[full];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4_t*>(&red[w][t][4 * lane]) = acc[t];
-  __syncthreads();
-  if (w < MT) {
-    f32x4_t sum = *reinterpret_cast<const f32x4_t*>(&red[0][w][4 * lane]);
+    for (int t = 0; t < T; ++t) {
+      const uint8_t* xt = xp[t % MT];
+      const uint4 z = make_uint4(0, 0, 0, 0), x0 = load(xt + o0), x1 = load(xt + o1);
+      const f32x4_t d = mfma128(load(wp[t / MT] + o0), load(wp[t / MT] + o1), in0 ? x0 : z, in1 ? x1 : z);
+      const float f = sx(t % MT, full) * sw;
 #pragma unroll
-    for (int i = 1; i < kSkWaves; ++i) {
-      const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&red[i][w][4 * lane]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += o[e];
+      for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], f, acc[t][e]);
     }
-    // Item e of lane (r, g): weight row 4 g + e, activation row r.
-    const int64_t i = i0 + 16 * w + r;
-    if (i < rows.count) {
-      uint16_t* dst = p.y + rows.out_row(i) * p.n + n0 + 4 * g;
+  }
+  // The sums of GT blocks at a time (what LDS holds of all wavefronts).
+  constexpr int GT = T < 4 ? T : 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n0 + 4 * g + e < p.n) dst[e] = (uint16_t)f32_to_bf16_rne(sum[e]);
+  for (int t0 = 0; t0 < T; t0 += GT) {
+    if (t0 > 0) __syncthreads();
+#pragma unroll
+    for (int t = 0; t < GT; ++t) red[(w * GT + t) * 64 + lane] = acc[t0 + t];
+    __syncthreads();
+    for (int tt = w; tt < GT; tt += waves) {
+      const int t = t0 + tt;
+      f32x4_t sum = red[tt * 64 + lane];
+      for (int i = 1; i < waves; ++i) {
+        const f32x4_t o = red[(i * GT + tt) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += o[e];
+      }
+      // Item e of lane (r, g): weight row 4 g + e, activation row r.
+      const int64_t i = i0 + 16 * (t % MT) + r, col = n0 + 16 * (t / MT) + 4 * g;
+      if (i >= rows.count || col >= p.n) continue;
+      uint16_t* dst = p.y + rows.out_row(i) * p.n + col;
+      if ((p.n & 3) == 0) {
+        const bf16x2_t lo = {(__bf16)sum[0], (__bf16)sum[1]}, hi = {(__bf16)sum[2], (__bf16)sum[3]};
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.n) dst[e] = (uint16_t)f32_to_bf16_rne(sum[e]);
+      }
     }
   }
 }
 
-template <int MT>
-__global__ void __launch_bounds__(64 * kSkWaves) fp8_skinny_kernel(SkinnyArgs p) {
-  __shared__ float red[kSkWaves][MT][256];
+template <int MT, int NT, int U, int MAXW, bool SXL>
+__global__ void __launch_bounds__(64 * MAXW) fp8_skinny_kernel(SkinnyArgs p) {
+  __shared__ f32x4_t red[MAXW * (MT * NT < 4 ? MT * NT : 4) * 64];
+  extern __shared__ float sxl[];
   const int64_t i0 = (int64_t)blockIdx.y * (16 * MT);
-  skinny_tile<MT>(p, p.wq, p.ws, (int64_t)blockIdx.x * 16, RowSpan{0, p.m, nullptr, 1}, i0, red);
+  skinny_tile<MT, NT, U, SXL>(p, p.wq, p.ws, (int64_t)blockIdx.x * (16 * NT), RowSpan{0, p.m, nullptr, 1}, i0,
+                         blockDim.x >> 6, red, sxl);
 }
 
 // Workgroup (x, y): 16 rows of W of the expert that owns tile y of the sort
 // (up to 128 pairs); past the last tile, rows of zeros for the pairs whose id
 // is out of range.
 template <int MT>
-__global__ void __launch_bounds__(64 * kSkWaves) fp8_skinny_grouped_kernel(SkinnyArgs p) {
-  __shared__ float red[kSkWaves][MT][256];
+__global__ void __launch_bounds__(512) fp8_skinny_grouped_kernel(SkinnyArgs p) {
+  __shared__ f32x4_t red[8 * MT * 64];
   const int32_t* pair_off = p.groups + p.experts;
   const int32_t* tile_off = p.groups + 2 * p.experts + 1;
   const int32_t* perm = p.groups + 3 * p.experts + 2;
@@ -139,7 +228,7 @@ __global__ void __launch_bounds__(64 * kSkWaves) fp8_skinny_grouped_kernel(Skinn
   const int64_t first = pair_off[lo] + (tile - tile_off[lo]) * 128, end = pair_off[lo + 1];
   const RowSpan rows{first, end - first < 128 ? end - first : 128, perm, p.topk};
   for (int64_t i0 = 0; i0 < rows.count; i0 += 16 * MT) {
-    skinny_tile<MT>(p, p.wq + lo * p.n * p.k, p.ws + lo * p.nb * p.kb, n0, rows, i0, red);
+    skinny_tile<MT, 1, 2, false>(p, p.wq + lo * p.n * p.k, p.ws + lo * p.nb * p.kb, n0, rows, i0, 8, red, nullptr);
     __syncthreads();
   }
 }
@@ -151,7 +240,13 @@ bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
   return n <= ((int64_t)1 << 26) && (m + 63) / 64 <= 65535 && k <= ((int64_t)1 << 37);
 }
 
-static bool use_gemm(int64_t m, int64_t n, int64_t k) { return m > 64 && fp8_gemm_supported(m, n, k); }
+// Few rows: the weight streams through registers.  From 33 rows on the reads of X
+// cost more than the GEMM's tiles, unless the weight is small (64 rows of X,
+// skinny against GEMM: 17408 x 5120 51.7 / 45.5 us, 5120 x 17408 77 / 38 us, 5120
+// x 5120 20 / 20 us, 1024 x 2048 7.3 us against two launches of 5).
+static bool use_gemm(int64_t m, int64_t n, int64_t k) {
+  return m > 32 && (m > 64 || n > ((int64_t)1 << 25) / k) && fp8_gemm_supported(m, n, k);
+}
 
 int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
@@ -162,13 +257,34 @@ bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64
          experts <= ((int64_t)1 << 28) && prefill_grouped_tile_bound(t_count * topk, experts) <= 65535;
 }
 
+// As few wavefronts as keep the number of passes over U blocks that MAXW allow.
+template <int MT, int NT, int U, int MAXW>
+static void launch_skinny_shape(const SkinnyArgs& a, hipStream_t s) {
+  const int passes = (a.kb + MAXW * U - 1) / (MAXW * U), waves = (a.kb + passes * U - 1) / (passes * U);
+  const dim3 grid((unsigned)((a.n + 16 * NT - 1) / (16 * NT)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT)));
+  const size_t lds = sizeof(float) * 16 * MT * (a.kb | 1);
+  if (lds <= 16384) fp8_skinny_kernel<MT, NT, U, MAXW, true><<<grid, 64 * waves, lds, s>>>(a);
+  else fp8_skinny_kernel<MT, NT, U, MAXW, false><<<grid, 64 * waves, 0, s>>>(a);
+}
+
 void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                        const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
   const SkinnyArgs a{xq, xs, wq, ws, y, m, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), nullptr, 1, 1};
-  const unsigned gx = (unsigned)((n + 15) / 16);
   if (use_gemm(m, n, k)) return launch_fp8_gemm(xq, xs, m, n, k, wq, ws, y, workspace, s);
-  if (m <= 16) fp8_skinny_kernel<1><<<dim3(gx, 1), 64 * kSkWaves, 0, s>>>(a);
-  else fp8_skinny_kernel<4><<<dim3(gx, (unsigned)((m + 63) / 64)), 64 * kSkWaves, 0, s>>>(a);
+  // Per shape: us at K = 5120 (N = 17408) / K = 17408 (N = 5120) / N = 1024, K = 2048.
+  if (m <= 16) {
+    // Two rows of blocks a wavefront read X half as often; few rows of W need
+    // every workgroup they can make.  M = 8: 24.2 / 26.3 / 5.6 against 28.6 / 33.2 / 4.5.
+    if (n > 2048) launch_skinny_shape<1, 2, 2, 4>(a, s);
+    else launch_skinny_shape<1, 1, 4, 8>(a, s);
+  } else if (m <= 32) {
+    // M = 32: 34.6 / 43.1 / 6.9, 36.2 / 37.0 / 7.1 and 41.1 / 54.0 / 6.1.
+    if (n <= 2048) launch_skinny_shape<2, 1, 2, 4>(a, s);
+    else if (k <= 8192) launch_skinny_shape<2, 2, 1, 8>(a, s);
+    else launch_skinny_shape<2, 2, 2, 4>(a, s);
+  } else {
+    launch_skinny_shape<2, 2, 1, 4>(a, s);
+  }
 }
 
 void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_count, int64_t topk, const int32_t* route,
@@ -180,7 +296,7 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
   const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), groups, experts,
                      topk};
   const dim3 grid((unsigned)((n + 15) / 16), (unsigned)prefill_grouped_tile_bound(pairs, experts));
-  fp8_skinny_grouped_kernel<2><<<grid, 64 * kSkWaves, 0, s>>>(a);
+  fp8_skinny_grouped_kernel<2><<<grid, 512, 0, s>>>(a);
 }
 
 }  // namespace nvfp4
