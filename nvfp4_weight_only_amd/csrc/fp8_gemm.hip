@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   // Lines brought into L2 ahead of their chunk's loads (one 4-byte read each, to
   // a part of LDS that nothing reads): the tiles that run on this XCD at the same
   // time and share rows of W (m tiles, up to 8) or of X share this work.
-  const int share_w = p.m_tiles < 8 ? p.m_tiles : 8, share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
+  const int share_w = GROUPED ? 1 : (p.m_tiles < 8 ? p.m_tiles : 8), share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
+  static_assert(!GROUPED || TN + TM <= 512, "one line per lane");
   const int lines_w = (TN + share_w - 1) / share_w, lines_x = (TM + share_x - 1) / share_x;
   const uint8_t* pf;
   {
@@ -497,6 +498,23 @@ bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) {
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = gemm_plan(m, n, k, true);
   return p.slices > 1 ? 4 * m * n * p.slices : 0;
+}
+
+bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
+  const int64_t pairs = t_count * topk, kb = (k + kChunk - 1) / kChunk;
+  return k <= ((int64_t)1 << 23) && t_count <= ((int64_t)UINT32_MAX) / k && t_count <= (int64_t)UINT32_MAX / 4 / kb &&
+         (pairs + 127) / 128 + experts <= ((int64_t)1 << 22) / ((n + 255) / 256);
+}
+
+void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,
+                             int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
+                             hipStream_t s) {
+  // Fewer than one tile past pairs / 128 for each expert that has pairs; at least
+  // one workgroup is left for rows of zeros if there are any.
+  const int64_t m_tiles = (pairs + 127) / 128 + (experts < pairs ? experts : pairs), n_tiles = (n + 255) / 256;
+  const GemmArgs a{xq, xs, wq, ws, y, pairs, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128),
+                   (int)n_tiles, (int)m_tiles, 1, nullptr, groups, experts, topk};
+  fp8_gemm_kernel<256, 128, 4, 2, 3, true><<<dim3((unsigned)(n_tiles * m_tiles)), 512, 0, s>>>(a);
 }
 
 void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,

@@ -31,21 +31,19 @@ struct SkinnyArgs {
   uint16_t* y;        // [m, n] ([pairs, n])
   int64_t m, n, k;    // m: rows of y
   int kb, nb;
-  // Routed form: the sort's int32 arrays, and pairs per token.
-  const int32_t* groups;
+  // Routed form: expert ids of the m pairs, and pairs per token.
+  const int32_t* route;
   int64_t experts, topk;
 };
 
 // The rows of y that a workgroup computes and where their activations are.
 struct RowSpan {
-  int64_t first, count;   // rows first .. first + count of the (sorted) pairs
-  const int32_t* perm;    // pair of a sorted row (nullptr: the row itself)
-  int64_t topk;
-  __device__ __forceinline__ int64_t out_row(int64_t i) const { return perm ? perm[first + i] : first + i; }
-  __device__ __forceinline__ int64_t x_row(int64_t i) const { return perm ? perm[first + i] / topk : first + i; }
+  int64_t count;
+  const int32_t* pairs;  // the rows of y (nullptr: 0, 1, ...)
+  uint32_t topk;         // rows of y per row of X
+  __device__ __forceinline__ int64_t out_row(int64_t i) const { return pairs ? pairs[i] : i; }
+  __device__ __forceinline__ int64_t x_row(int64_t i) const { return pairs ? (uint32_t)pairs[i] / topk : i; }
 };
-
-constexpr int kMaxWaves = 16;
 
 // 16 NT rows of W against 16 MT rows of X by a workgroup of `waves` wavefronts,
 // each of which takes a contiguous share of the whole blocks of K, U blocks at a
@@ -199,37 +197,43 @@ __global__ void __launch_bounds__(64 * MAXW) fp8_skinny_kernel(SkinnyArgs p) {
   __shared__ f32x4_t red[MAXW * (MT * NT < 4 ? MT * NT : 4) * 64];
   extern __shared__ float sxl[];
   const int64_t i0 = (int64_t)blockIdx.y * (16 * MT);
-  skinny_tile<MT, NT, U, SXL>(p, p.wq, p.ws, (int64_t)blockIdx.x * (16 * NT), RowSpan{0, p.m, nullptr, 1}, i0,
+  skinny_tile<MT, NT, U, SXL>(p, p.wq, p.ws, (int64_t)blockIdx.x * (16 * NT), RowSpan{p.m, nullptr, 1}, i0,
                          blockDim.x >> 6, red, sxl);
 }
 
-// Workgroup (x, y): 16 rows of W of the expert that owns tile y of the sort
-// (up to 128 pairs); past the last tile, rows of zeros for the pairs whose id
-// is out of range.
-template <int MT>
-__global__ void __launch_bounds__(512) fp8_skinny_grouped_kernel(SkinnyArgs p) {
-  __shared__ f32x4_t red[8 * MT * 64];
-  const int32_t* pair_off = p.groups + p.experts;
-  const int32_t* tile_off = p.groups + 2 * p.experts + 1;
-  const int32_t* perm = p.groups + 3 * p.experts + 2;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, tile = blockIdx.y, tiles = tile_off[p.experts];
-  if (tile >= tiles) {
-    const int64_t valid = pair_off[p.experts], spare = gridDim.y - tiles;
-    for (int64_t i = valid + tile - tiles; i < p.m; i += spare)
-      if (threadIdx.x < 16 && n0 + threadIdx.x < p.n) p.y[perm[i] * p.n + n0 + threadIdx.x] = 0;
+// Few pairs over an expert stack, without a sort: workgroup (x, p) multiplies 16
+// NT rows of W of pair p's expert with the activations of every pair that chose
+// that expert, if p is the first of them (the others' workgroups end); a pair
+// whose id is out of range gets zeros.  The order in which the pairs are found
+// varies; every output depends on its own rows only.
+constexpr int kMaxPairs = 1024;
+
+template <int MT, int NT, int U, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
+  __shared__ f32x4_t red[WAVES * (MT * NT < 4 ? MT * NT : 4) * 64];
+  __shared__ int32_t same[kMaxPairs];
+  __shared__ int32_t count, earlier;
+  const int pair = blockIdx.y, pairs = (int)p.m;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+  const int32_t id = p.route[pair];
+  if (id < 0 || id >= p.experts) {
+    for (int c = threadIdx.x; c < 16 * NT && n0 + c < p.n; c += blockDim.x) p.y[pair * p.n + n0 + c] = 0;
     return;
   }
-  int64_t lo = 0, hi = p.experts - 1;  // the expert with tile_off[e] <= tile < tile_off[e + 1]
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (tile_off[mid] <= tile) lo = mid;
-    else hi = mid - 1;
+  if (threadIdx.x == 0) count = 0, earlier = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    if (p.route[i] != id) continue;
+    if (i < pair) earlier = 1;
+    else same[atomicAdd(&count, 1)] = i;
   }
-  const int64_t first = pair_off[lo] + (tile - tile_off[lo]) * 128, end = pair_off[lo + 1];
-  const RowSpan rows{first, end - first < 128 ? end - first : 128, perm, p.topk};
+  __syncthreads();
+  if (earlier) return;
+  const RowSpan rows{count, same, (uint32_t)p.topk};
   for (int64_t i0 = 0; i0 < rows.count; i0 += 16 * MT) {
-    skinny_tile<MT, 1, 2, false>(p, p.wq + lo * p.n * p.k, p.ws + lo * p.nb * p.kb, n0, rows, i0, 8, red, nullptr);
-    __syncthreads();
+    if (i0 > 0) __syncthreads();  // red is free again
+    skinny_tile<MT, NT, U, false>(p, p.wq + id * p.n * p.k, p.ws + (int64_t)id * p.nb * p.kb, n0, rows, i0, WAVES, red,
+                                  nullptr);
   }
 }
 
@@ -252,9 +256,15 @@ int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
 }
 
+// The GEMM's tiles: 128 pairs each, the last of an expert with fewer.
+static bool use_routed(int64_t pairs, int64_t experts, int64_t n) {
+  return pairs <= kMaxPairs && pairs <= 16 * experts && n <= ((int64_t)1 << 26);
+}
+
 bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
-  return fp8_linear_supported(1, n, k) && topk <= ((int64_t)1 << 30) / t_count &&
-         experts <= ((int64_t)1 << 28) && prefill_grouped_tile_bound(t_count * topk, experts) <= 65535;
+  if (topk > ((int64_t)1 << 30) / t_count || experts > ((int64_t)1 << 28)) return false;
+  return use_routed(t_count * topk, experts, n) ? k <= ((int64_t)1 << 37)
+                                                : fp8_gemm_grouped_supported(t_count, topk, experts, n, k);
 }
 
 // As few wavefronts as keep the number of passes over U blocks that MAXW allow.
@@ -291,12 +301,16 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
                                int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
                                void* workspace, hipStream_t s) {
   const int64_t pairs = t_count * topk;
+  if (use_routed(pairs, experts, n)) {
+    const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), route, experts,
+                       topk};
+    const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pairs);
+    fp8_routed_kernel<1, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+    return;
+  }
   int32_t* groups = static_cast<int32_t*>(workspace);
   launch_group_sort(route, pairs, experts, groups, s);
-  const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), groups, experts,
-                     topk};
-  const dim3 grid((unsigned)((n + 15) / 16), (unsigned)prefill_grouped_tile_bound(pairs, experts));
-  fp8_skinny_grouped_kernel<2><<<grid, 512, 0, s>>>(a);
+  launch_fp8_gemm_grouped(xq, xs, topk, groups, pairs, experts, n, k, wq, ws, y, s);
 }
 
 }  // namespace nvfp4

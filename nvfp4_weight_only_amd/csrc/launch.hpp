@@ -157,6 +157,11 @@ bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k);
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
 void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                      const float* ws, uint16_t* y, void* workspace, hipStream_t s);
+// The GEMM over the pairs sorted by expert (launch_group_sort).
+bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k);
+void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,
+                             int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
+                             hipStream_t s);
 bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k);
 void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_count, int64_t topk, const int32_t* route,
                                int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
