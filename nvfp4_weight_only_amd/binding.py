@@ -110,8 +110,18 @@ def _check(status: int, what: str) -> None:
         raise NVFP4Error(status, what)
 
 
+# The current stream's handle without building a torch.cuda.Stream (0.1 us instead of 1.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: torch.device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _stream_of(t.device)
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
@@ -631,10 +641,10 @@ def _need_codes(t: torch.Tensor, name: str) -> None:
 def _call(fn, what: str, device: torch.device, *args) -> None:
     """fn(*args, stream) on `device` and its current stream, whichever device is the current one."""
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+        _check(fn(*args, _stream_of(device)), what)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+            _check(fn(*args, _stream_of(device)), what)
 
 
 def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
