@@ -19,13 +19,13 @@ struct Fp8Sizes {
 
 nvfp4_status fp8_sizes(int64_t count, int64_t rows, int64_t k, int64_t block_rows, Fp8Sizes* s) {
   if (count < 0 || rows < 0 || k <= 0 || (k & 15) != 0) return NVFP4_ERR_SHAPE;
-  int64_t all, row_blocks;
+  int64_t all;
   if (!mul_ok(count, rows, &all) || !mul_ok(all, k, &s->codes) || !mul_ok(s->codes, 4, &s->bf16))
     return NVFP4_ERR_SHAPE;
   s->bf16 = 2 * s->codes;
-  // blocks <= elements, and 4 bytes of scale per block: no overflow past the check above.
-  row_blocks = rows / block_rows + (rows % block_rows != 0);
-  s->scales = 4 * count * row_blocks * (k / 128 + (k % 128 != 0));
+  // At most one block per element, so 4 bytes of scale each do not overflow past the check above.
+  const int64_t row_blocks = rows / block_rows + (rows % block_rows != 0);
+  s->scales = s->codes == 0 ? 0 : 4 * count * row_blocks * (k / 128 + (k % 128 != 0));
   return NVFP4_OK;
 }
 

@@ -239,17 +239,17 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
 
 }  // namespace
 
-// 16 rows of W per workgroup along x (at most 2^32 threads), 64 rows of X along y.
-bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
-  return n <= ((int64_t)1 << 26) && (m + 63) / 64 <= 65535 && k <= ((int64_t)1 << 37);
-}
-
 // Few rows: the weight streams through registers.  From 33 rows on the reads of X
 // cost more than the GEMM's tiles, unless the weight is small (64 rows of X,
 // skinny against GEMM: 17408 x 5120 51.7 / 45.5 us, 5120 x 17408 77 / 38 us, 5120
 // x 5120 20 / 20 us, 1024 x 2048 7.3 us against two launches of 5).
 static bool use_gemm(int64_t m, int64_t n, int64_t k) {
   return m > 32 && (m > 64 || n > ((int64_t)1 << 25) / k) && fp8_gemm_supported(m, n, k);
+}
+
+// Otherwise 16 or 32 rows of W per workgroup along x, at least 16 of X along y.
+bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
+  return use_gemm(m, n, k) || (n <= ((int64_t)1 << 26) && m <= 16 * 65535 && k <= ((int64_t)1 << 37));
 }
 
 int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {

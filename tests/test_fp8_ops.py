@@ -443,3 +443,206 @@ def test_fp8_linear_grouped(nv, t, topk, e, n, k, kind):
     dirty = torch.full((nv.fp8_linear_grouped_workspace_bytes(t, topk, e),), 0xAB, dtype=torch.uint8, device="cuda")
     out = torch.full_like(y, 3.0)
     assert torch.equal(nv.fp8_linear_grouped(*d, out=out, workspace=dirty), y)
+
+
+# ---------------------------------------------------------------------------
+# The operators together, and how they are called.
+# ---------------------------------------------------------------------------
+def mlp(nv, x, r, g, gu, down):
+    """One MLP block in E4M3: residual + norm -> gate/up -> silu * up -> down; (y, new residual)."""
+    q, s, h = nv.rmsnorm_fp8(x, g, EPS, residual=r)
+    q, s = nv.silu_mul_fp8(nv.fp8_linear(q, s, *gu))
+    return nv.fp8_linear(q, s, *down), h
+
+
+def close(got, want, tol):
+    """Relative 2-norm; the chain's own roundings: E4M3 (2^-4 a value at most) in two operands that both sides round
+    alike up to the BF16 rounding between them (2^-8), which moves few codes by a step."""
+    got, want = got.double(), want.double()
+    assert float((got - want).norm()) <= tol * float(want.norm())
+
+
+def chain_inputs(m, k, n, seed, e=None):
+    lead = () if e is None else (e,)
+    x, r = bf16(WL.normal_bf16((m, k), 1.0, seed)), bf16(WL.normal_bf16((m, k), 2.0, seed + 1))
+    g = bf16(WL.normal_bf16((k,), 1.0, seed + 2))
+    gu, down = bf16(WL.normal_bf16(lead + (2 * n, k), 0.05, seed + 3)), bf16(WL.normal_bf16(lead + (k, n), 0.05, seed + 4))
+    return x, r, g, gu, down
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k,n", [(1, 512, 384), (7, 1040, 400), (150, 512, 1024), (300, 2048, 1040)])
+def test_fp8_mlp_block(nv, m, k, n):
+    """The operators in a row against the same steps in float64, with the operands rounded to E4M3 by the oracle's
+    definition and BF16 between the steps."""
+    x, r, g, gu, down = chain_inputs(m, k, n, 900 + m)
+    guq, dq = nv.fp8_quantize(gu, 128), nv.fp8_quantize(down, 128)
+    y, h = mlp(nv, x, r, g, guq, dq)
+    hd = host((x.float() + r.float()).bfloat16())
+    assert np.array_equal(host(h), hd)
+    cq, cs = F.norm(hd, host(g), EPS)
+    a, _ = F.linear(cq, cs, *F.quantize(host(gu), 128))
+    a = torch.from_numpy(a).bfloat16().double().numpy()
+    q, s = F.quantize(F.silu_mul(a[:, :n], a[:, n:]), 1)
+    want, _ = F.linear(q, s, *F.quantize(host(down), 128))
+    # gate/up outputs: 2^-8 rounding on both sides and the products' 7 2^-13 of sum |x w|; at most a code step (2^-3)
+    # where they move a value over a border, which a share of about 2^-8 / 2^-4 of the values is near to.
+    close(y.cpu(), torch.from_numpy(want), 2.0 ** -8 + 2.0 ** -3 * (2.0 ** -4) ** 0.5)
+
+
+@pytest.mark.gpu
+def test_fp8_moe_block(nv):
+    """norm -> grouped gate/up -> silu * up -> grouped down (one row per pair), with padding tokens: row for row the
+    same bits as the dense operators on each expert's rows."""
+    t, topk, e, k, n = 37, 2, 5, 512, 272
+    x, r, g, gu, down = chain_inputs(t, k, n, 950, e)
+    guq, dq = nv.fp8_quantize(gu, 128), nv.fp8_quantize(down, 128)
+    route = routing("uniform", t, topk, e, 951)
+    route[30:] = -1
+    rd = dev(route)
+    q, s, h = nv.rmsnorm_fp8(x, g, EPS, residual=r)
+    a = nv.fp8_linear_grouped(q, s, rd, *guq)
+    q2, s2 = nv.silu_mul_fp8(a.view(t * topk, 2 * n))
+    y = nv.fp8_linear_grouped(q2, s2, rd.view(t * topk, 1), *dq).view(t, topk, k)
+    valid = (route >= 0) & (route < e)
+    assert not host(y)[~valid].any() and not host(a)[~valid].any()
+    ra, ba = F.linear_routed(host(q), host(s), route, host(guq[0]), host(guq[1]))
+    check(a, ra, ba, k)
+    ry, by = F.linear_routed(host(q2), host(s2), route.reshape(-1, 1), host(dq[0]), host(dq[1]))
+    check(y, ry.reshape(t, topk, k), by.reshape(t, topk, k), n)
+
+
+@pytest.mark.gpu
+def test_fp8_graph_replays_match_eager(nv):
+    """A whole MLP and MoE step captured once and replayed with other work in between, on new inputs too; two graphs
+    captured on one stream keep apart."""
+    x, r, g, gu, down = chain_inputs(260, 512, 1024, 970)
+    guq, dq = nv.fp8_quantize(gu, 128), nv.fp8_quantize(down, 128)
+    stack = nv.fp8_quantize(bf16(WL.normal_bf16((6, 272, 512), 0.05, 975)), 128)
+    routes = [dev(routing("skew", 260, 4, 6, 976)), dev(routing("uniform", 3, 2, 6, 977))]
+    long_w = nv.fp8_quantize(bf16(WL.normal_bf16((304, 8192), 0.05, 978)), 128)
+    long_x = nv.fp8_quantize(bf16(WL.normal_bf16((260, 8192), 1.0, 979)))
+    assert nv.fp8_linear_workspace_bytes(260, 304, 8192) > 0      # K split: two launches and a workspace
+
+    def step():
+        q, s, h = nv.rmsnorm_fp8(x, g, EPS, residual=r)
+        y, _ = mlp(nv, x, r, g, guq, dq)
+        few = nv.fp8_linear_grouped(q[:3].contiguous(), s[:3].contiguous(), routes[1], *stack)
+        return [h, y, nv.fp8_linear_grouped(q, s, routes[0], *stack), few, nv.fp8_linear(*long_x, *long_w),
+                nv.fp8_linear(q[:5].contiguous(), s[:5].contiguous(), *guq), *nv.fp8_quantize(x, 128)]
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            out = step()
+        graphs.append((gr, out))
+    torch.cuda.synchronize()
+    for rep in range(3):
+        x.copy_(bf16(WL.normal_bf16((260, 512), 1.0, 980 + rep)))
+        want = step()
+        torch.cuda.synchronize()
+        for gr, out in graphs:
+            for o in out:
+                o.zero_()
+        torch.cuda.synchronize()
+        for gr, _ in graphs:
+            gr.replay()
+        step()                                                     # eager work beside the replays
+        torch.cuda.synchronize()
+        for i, (_, out) in enumerate(graphs):
+            for j, (o, ref) in enumerate(zip(out, want)):
+                assert torch.equal(o.view(torch.uint8), ref.view(torch.uint8)), (rep, i, j)
+
+
+@pytest.mark.gpu
+def test_fp8_two_streams_at_once(nv):
+    """Calls in flight on two streams, each with its own workspace, give the results of one after the other."""
+    w = [nv.fp8_quantize(bf16(WL.normal_bf16((304, 8192), 0.05, 990 + i)), 128) for i in range(2)]
+    x = [nv.fp8_quantize(bf16(WL.normal_bf16((260, 8192), 1.0, 992 + i))) for i in range(2)]
+    want = [nv.fp8_linear(*x[i], *w[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(nv.fp8_linear(*x[i], *w[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in got[i]:
+            assert torch.equal(y, want[i])
+
+
+@pytest.mark.gpu
+def test_fp8_binding_refusals(nv):
+    x = bf16(WL.normal_bf16((4, 256), 1.0, 1000))
+    g = bf16(WL.normal_bf16((256,), 1.0, 1001))
+    q, s = nv.fp8_quantize(x)
+    wq, ws = nv.fp8_quantize(bf16(WL.normal_bf16((64, 256), 1.0, 1002)), 128)
+    route = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: nv.fp8_quantize(x.float()), lambda: nv.fp8_quantize(x.cpu()), lambda: nv.fp8_quantize(x[:, ::2]),
+        lambda: nv.fp8_quantize(x[0]), lambda: nv.fp8_quantize(x, 64), lambda: nv.fp8_quantize(x[:, :8].contiguous()),
+        lambda: nv.rmsnorm_fp8(x, g[:128].contiguous()), lambda: nv.rmsnorm_fp8(x, g, residual_out=x),
+        lambda: nv.rmsnorm_fp8(x, g, residual=x[:2]), lambda: nv.rmsnorm_fp8(x, g.float()),
+        lambda: nv.silu_mul_fp8(x[0]), lambda: nv.silu_mul_fp8(x[:, :255].contiguous()),
+        lambda: nv.silu_mul_fp8(x[:, :16].contiguous()),
+        lambda: nv.fp8_linear(q, s[:2].contiguous(), wq, ws), lambda: nv.fp8_linear(q.int(), s, wq, ws),
+        lambda: nv.fp8_linear(q, s, wq[:, :128].contiguous(), ws), lambda: nv.fp8_linear(q, s, wq, ws.double()),
+        lambda: nv.fp8_linear(q, s, wq, ws, out=x), lambda: nv.fp8_linear(q, s, wq, ws, workspace="none"),
+        lambda: nv.fp8_linear(q, s, wq.cpu(), ws),
+        lambda: nv.fp8_linear_grouped(q, s, route, wq, ws), lambda: nv.fp8_linear_grouped(q, s, route[:2], wq[None], ws[None]),
+        lambda: nv.fp8_linear_grouped(q, s, route.long(), wq[None], ws[None]),
+        lambda: nv.fp8_linear_grouped(q, s, route[:, :0], wq[None], ws[None]),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was not refused")
+    with pytest.raises(nv.NVFP4Error):
+        nv.rmsnorm_fp8(x, g, 0.0)
+    with pytest.raises(nv.NVFP4Error):
+        nv.rmsnorm_fp8(x, g, residual=x, residual_out=x)           # over the input
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(nv.NVFP4Error):
+        nv.fp8_linear_grouped(q, s, route, wq[None].contiguous(), ws[None].contiguous(), workspace=small)
+    # empty batches
+    assert nv.fp8_quantize(x[:0])[0].shape == (0, 256) and nv.silu_mul_fp8(x[:0])[1].shape == (0, 1)
+    assert nv.rmsnorm_fp8(x[:0], g, residual=x[:0])[2].shape == (0, 256)
+    assert nv.fp8_linear(q[:0], s[:0], wq, ws).shape == (0, 64)
+    assert nv.fp8_linear_grouped(q[:0], s[:0], route[:0], wq[None], ws[None]).shape == (0, 2, 64)
+
+
+def test_fp8_binding_refuses_mixed_devices():
+    class On:
+        def __init__(self, device):
+            self.device = torch.device(device)
+    assert B._one_device(On("cuda:1"), None, On("cuda:1")) == torch.device("cuda:1")
+    with pytest.raises(ValueError, match="different devices"):
+        B._one_device(On("cuda:0"), On("cuda:1"))
+
+
+def test_fp8_binding_runs_on_the_tensors_device(monkeypatch):
+    """A call whose tensors are on another device than the current one switches to it and takes its stream."""
+    seen = []
+    now = {"dev": 0}
+
+    class Guard:
+        def __init__(self, device):
+            self.to = device.index
+
+        def __enter__(self):
+            self.before, now["dev"] = now["dev"], self.to
+
+        def __exit__(self, *a):
+            now["dev"] = self.before
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now["dev"])
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(B, "_stream_of", lambda d: 100 + d.index)
+    for index in (0, 1):
+        B._call(lambda *a: seen.append((now["dev"], a)) or 0, "f", torch.device("cuda", index), 7)
+    assert seen == [(0, (7, 100)), (1, (7, 101))] and now["dev"] == 0
