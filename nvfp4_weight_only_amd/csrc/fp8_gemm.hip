@@ -25,7 +25,9 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) const void lds_t;
 
 constexpr int kChunk = 128;
-// How many chunks ahead of the loads to LDS lines are brought into L2.
+// Tiles with two stages only: how many chunks ahead of the loads to LDS lines are
+// brought into L2 (256 x 256 over 2048 x 16384 x 5120: 174 us without, 170 with;
+// deeper rings lose 5 to 15 % by it).
 constexpr int kAhead = 2;
 
 struct GemmArgs {
@@ -119,11 +121,11 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   static_assert(WN * WM == 8 && TN % (32 * WN) == 0 && TM % (16 * WM) == 0 && TN % 64 == 0 && TM % 64 == 0, "tile");
   constexpr int NT = TN / WN / 16, MT = TM / WM / 16, T = NT * MT;  // 16 x 16 blocks of a wavefront
   static_assert(T % 4 == 0 && NT % 2 == 0 && MT >= 2 && 128 % (TN / WN) == 0, "register rings; one scale of W");
-  constexpr int LW = TN / 64, LX = TM / 64, NL = LW + LX + 2;  // loads per wavefront and chunk
+  constexpr int LW = TN / 64, LX = TM / 64, L2 = ST == 2, NL = LW + LX + 1 + L2;  // loads per wavefront and chunk
   constexpr int QJ = NL <= T ? 1 : 2;  // loads behind each matrix instruction
   static_assert(NL <= QJ * T, "a chunk's loads are issued before the next barrier");
   __shared__ Stage<TN, TM> stage[ST];
-  __shared__ uint32_t sink[64];
+  __shared__ uint32_t sink[L2 ? 64 : 1];
   static_assert(sizeof(stage) >= sizeof(uint16_t) * TN * TM, "the epilogue's tile fits the stages");
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -200,11 +202,11 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   // Lines brought into L2 ahead of their chunk's loads (one 4-byte read each, to
   // a part of LDS that nothing reads): the tiles that run on this XCD at the same
   // time and share rows of W (m tiles, up to 8) or of X share this work.
-  const int share_w = GROUPED ? 1 : (p.m_tiles < 8 ? p.m_tiles : 8), share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
-  static_assert(!GROUPED || TN + TM <= 512, "one line per lane");
-  const int lines_w = (TN + share_w - 1) / share_w, lines_x = (TM + share_x - 1) / share_x;
-  const uint8_t* pf;
-  {
+  static_assert(!L2 || (!GROUPED && TN + TM <= 512), "one line per lane");
+  const uint8_t* pf = nullptr;
+  if constexpr (L2) {
+    const int share_w = p.m_tiles < 8 ? p.m_tiles : 8, share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
+    const int lines_w = (TN + share_w - 1) / share_w, lines_x = (TM + share_x - 1) / share_x;
     const int i = 8 * lane + w;
     if (i < lines_w || i >= lines_w + lines_x) {
       const int r = (i < lines_w ? i : 0) * share_w + mt % share_w;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
       if (i < NT - 1) {
         a[(i + 1) & 1] = read(so + rw, i + 1);
       } else {
-        wait_loads<(ST - 2) * NL + 1>();
+        wait_loads<(ST - 2) * NL + L2>();
         finish(c + 1, sidx);
         meet();
         a[0] = read(sn + rw, 0);
@@ -424,7 +426,7 @@ struct Shape {
   double chunk, tile;
 };
 constexpr Shape kShapes[4] = {
-    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1150, 7000}, {128, 64, 2, 1150, 7000}, {256, 64, 1, 1200, 7000}};
+    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 7000}, {256, 64, 1, 1100, 7000}};
 constexpr int kCus = 256;
 
 int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
@@ -433,7 +435,7 @@ int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) 
 double shape_ns(const Shape& s, int64_t wgs, int64_t chunks) {
   const int64_t slots = (int64_t)kCus * s.per_cu;
   // Half-filled CUs: a workgroup alone on its CU takes a little under half the pair's time.
-  if (s.per_cu == 2 && wgs <= kCus) return s.tile + 480.0 * (double)chunks;
+  if (s.per_cu == 2 && wgs <= kCus) return s.tile + 400.0 * (double)chunks;
   return (double)((wgs + slots - 1) / slots) * (s.tile + s.chunk * (double)chunks);
 }
 
