@@ -663,11 +663,6 @@ def _fp8_k(k: int) -> None:
         raise ValueError(f"the last dimension must be a positive multiple of 16, got {k}")
 
 
-def _fp8_outputs(lead, rows: int, k: int, block_rows: int, device: torch.device):
-    return (torch.empty((*lead, rows, k), dtype=torch.uint8, device=device),
-            torch.empty((*lead, -(-rows // block_rows), _fp8_blocks(k)), dtype=torch.float32, device=device))
-
-
 def fp8_quantize(w: torch.Tensor, block_rows: int = 1) -> Tuple[torch.Tensor, torch.Tensor]:
     """BF16 [n, k] or [e, n, k] -> (codes uint8 of the same shape, scales float32 [..., ceil(n/block_rows),
     ceil(k/128)]): E4M3 with one scale per block_rows x 128 block, block_rows 1 (activations) or 128 (weights)."""
@@ -678,7 +673,8 @@ def fp8_quantize(w: torch.Tensor, block_rows: int = 1) -> Tuple[torch.Tensor, to
         raise ValueError(f"block_rows must be 1 or {_FP8_BLOCK}, got {block_rows}")
     lead, (n, k) = tuple(w.shape[:-2]), w.shape[-2:]
     _fp8_k(k)
-    codes, scales = _fp8_outputs(lead, n, k, block_rows, w.device)
+    codes = torch.empty_like(w, dtype=torch.uint8)
+    scales = torch.empty((*lead, -(-n // block_rows), _fp8_blocks(k)), dtype=torch.float32, device=w.device)
     _call(lib().nvfp4_fp8_quantize, "nvfp4_fp8_quantize", w.device, w.data_ptr(), lead[0] if lead else 1, n, k,
           block_rows, codes.data_ptr(), scales.data_ptr())
     return codes, scales
@@ -709,7 +705,8 @@ def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
         if residual.shape != x.shape or residual_out.shape != x.shape:
             raise ValueError("residual and residual_out must have x's shape")
     device = _one_device(x, weight, residual, residual_out)
-    codes, scales = _fp8_outputs((), m, k, 1, device)
+    codes = torch.empty_like(x, dtype=torch.uint8)
+    scales = torch.empty((m, _fp8_blocks(k)), dtype=torch.float32, device=device)
     _call(lib().nvfp4_rmsnorm_fp8, "nvfp4_rmsnorm_fp8", device, x.data_ptr(),
           None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, m, k,
           None if residual is None else residual_out.data_ptr(), codes.data_ptr(), scales.data_ptr())
@@ -724,7 +721,8 @@ def silu_mul_fp8(gate_up: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         raise ValueError("gate_up must be [m, 2n]")
     m, n = gate_up.shape[0], gate_up.shape[1] // 2
     _fp8_k(n)
-    codes, scales = _fp8_outputs((), m, n, 1, gate_up.device)
+    codes = torch.empty((m, n), dtype=torch.uint8, device=gate_up.device)
+    scales = torch.empty((m, _fp8_blocks(n)), dtype=torch.float32, device=gate_up.device)
     _call(lib().nvfp4_silu_mul_fp8, "nvfp4_silu_mul_fp8", gate_up.device, gate_up.data_ptr(), m, n, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales

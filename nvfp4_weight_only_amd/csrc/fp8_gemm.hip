@@ -426,20 +426,26 @@ struct Shape {
   double chunk, tile;
 };
 constexpr Shape kShapes[4] = {
-    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 7000}, {256, 64, 1, 1100, 7000}};
+    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 5500}, {256, 64, 1, 1100, 7000}};
 constexpr int kCus = 256;
 
 int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
 
-// Estimated ns of the tiles over the chip, each K slice `chunks` long.
-double shape_ns(const Shape& s, int64_t wgs, int64_t chunks) {
-  const int64_t slots = (int64_t)kCus * s.per_cu;
-  // Half-filled CUs: a workgroup alone on its CU takes a little under half the pair's time.
-  if (s.per_cu == 2 && wgs <= kCus) return s.tile + 400.0 * (double)chunks;
-  return (double)((wgs + slots - 1) / slots) * (s.tile + s.chunk * (double)chunks);
+// Estimated ns of the tiles over the chip, each K slice `chunks` long.  A chunk
+// takes its compute time or that of its loads: 21 ns per KB that L2 holds, 43 per
+// KB from HBM, where W comes from for one of the m tiles.
+double shape_ns(const Shape& s, int64_t m, int64_t wgs, int64_t chunks) {
+  const double m_tiles = (double)((m + s.tm - 1) / s.tm), slots = (double)kCus * s.per_cu;
+  const double loads = 0.125 * (s.tn * (21.0 + 22.0 / m_tiles) + 21.0 * s.tm);
+  // Half-filled CUs: a workgroup alone on its CU computes in a little under half the pair's time.
+  const bool alone = s.per_cu == 2 && wgs <= kCus;
+  const double compute = alone ? 400.0 : s.chunk, load = s.per_cu == 2 && !alone ? 2.0 * loads : loads;
+  const double rounds = (double)((wgs + (int64_t)slots - 1) / (int64_t)slots);
+  return rounds * (s.tile + (compute > load ? compute : load) * (double)chunks);
 }
 
 struct Plan {
+  double ns = 1e300;
   int shape = 0, slices = 1;
   int64_t n1 = 0;  // columns of the 256 x 256 tiles that come first (0: one launch)
 };
@@ -451,24 +457,23 @@ struct Plan {
 Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
   const int64_t chunks = (k + kChunk - 1) / kChunk;
   Plan best;
-  double cost = 1e300;
   for (int i = 0; i < 4; ++i) {
     const int64_t tiles = tiles_of(kShapes[i], m, n);
     for (int s = 1; s <= 8; ++s) {
       if (s > 1 && (!split || (n & 3) != 0 || chunks < 4 * s || tiles * s > 2 * kCus ||
                     m * n > ((int64_t)1 << 26) / s))
         break;
-      const double ns = shape_ns(kShapes[i], tiles * s, (chunks + s - 1) / s) +
-                        (s > 1 ? 5000.0 + 8.0 * (double)(m * n) * s / 4000.0 : 0.0);
-      if (ns < cost) cost = ns, best = Plan{i, s, 0};
+      const double ns = shape_ns(kShapes[i], m, tiles * s, (chunks + s - 1) / s) +
+                        (s > 1 ? 1500.0 + 8.0 * (double)(m * n) * s / 4000.0 : 0.0);
+      if (ns < best.ns) best = Plan{ns, i, s, 0};
     }
   }
   const int64_t m_tiles = (m + 255) / 256, n_tiles = (n + 255) / 256;
   const int64_t rounds = n_tiles * m_tiles / kCus, cols = rounds * kCus / m_tiles;  // n tiles of whole rounds
   if (rounds > 0 && cols > 0 && cols < n_tiles) {
-    const double ns = shape_ns(kShapes[0], cols * m_tiles, chunks) + 3000.0 +
-                      shape_ns(kShapes[2], tiles_of(kShapes[2], m, n - 256 * cols), chunks);
-    if (ns < cost) best = Plan{0, 1, 256 * cols};
+    const double ns = shape_ns(kShapes[0], m, cols * m_tiles, chunks) + 3000.0 +
+                      shape_ns(kShapes[2], m, tiles_of(kShapes[2], m, n - 256 * cols), chunks);
+    if (ns < best.ns) best = Plan{ns, 0, 1, 256 * cols};
   }
   return best;
 }
@@ -496,6 +501,8 @@ void launch_shape(int shape, const GemmArgs& a, hipStream_t s) {
 bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) {
   return k <= ((int64_t)1 << 23) && (m + 63) / 64 <= ((int64_t)1 << 22) / ((n + 127) / 128);
 }
+
+double fp8_gemm_ns(int64_t m, int64_t n, int64_t k) { return gemm_plan(m, n, k, true).ns; }
 
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = gemm_plan(m, n, k, true);

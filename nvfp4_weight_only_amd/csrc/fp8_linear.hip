@@ -7,7 +7,6 @@
 // operand (columns m), so the four results of a lane belong to one activation
 // row: one factor xs[m, b] ws[n / 128, b] per lane.  Both operands place the
 // same element of K at the same position, whatever the order within the block.
-#include <type_traits>
 
 #include "device_common.hpp"
 #include "launch.hpp"
@@ -31,6 +30,7 @@ struct SkinnyArgs {
   uint16_t* y;        // [m, n] ([pairs, n])
   int64_t m, n, k;    // m: rows of y
   int kb, nb;
+  int span;           // rows of W per workgroup, a multiple of 4
   // Routed form: expert ids of the m pairs, and pairs per token.
   const int32_t* route;
   int64_t experts, topk;
@@ -50,19 +50,26 @@ struct RowSpan {
 // time, with the next U blocks of W already on their way; the last wavefront
 // adds the last, short block.  Their sums meet in LDS and are added in wavefront
 // order.  SXL: the rows' scales are first copied to LDS.
+constexpr int sums_at_a_time(int t) { return t <= 10 ? t : (t + 1) / 2; }
+
 template <int MT, int NT, int U, bool SXL>
 __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* wq, const float* ws, int64_t n0,
                                             const RowSpan& rows, int64_t i0, int waves, f32x4_t* red, float* sxl) {
   constexpr int T = MT * NT;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n1 = n0 + p.span < p.n ? n0 + p.span : p.n;  // past the last row of W
   const uint8_t* wp[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int64_t wr = n0 + 16 * t + r < p.n ? n0 + 16 * t + r : p.n - 1;
+    const int64_t wr = n0 + 16 * t + r < n1 ? n0 + 16 * t + r : n1 - 1;
     wp[t] = wq + wr * p.k + 16 * g;
   }
+  // The rows of W lie in one block of 128 or two: quad 4 g of rows of W (the
+  // rows of this lane's results) in the second one from block t on.
   const float* wsp = ws + (n0 >> 7) * p.kb;
+  const float* wsp2 = ws + ((n1 - 1) >> 7) * p.kb;
+  const int rest = 128 - (int)(n0 & 127);
   const uint8_t* xp[MT];
   const float* xsp[MT];
 #pragma unroll
@@ -73,14 +80,6 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
     xsp[t] = p.xs + xr * p.kb;
   }
   const int ld = p.kb | 1;  // an odd number of words from row to row
-  if constexpr (SXL) {
-    for (int i = threadIdx.x; i < 16 * MT * p.kb; i += blockDim.x) {
-      const int rr = i / p.kb, c = i - rr * p.kb;
-      const int64_t xi = i0 + rr < rows.count ? i0 + rr : rows.count - 1;
-      sxl[rr * ld + c] = p.xs[rows.x_row(xi) * p.kb + c];
-    }
-    __syncthreads();
-  }
   const auto sx = [&](int t, int b) -> float { return SXL ? sxl[(16 * t + r) * ld + b] : xsp[t][b]; };
   const auto load = [](const uint8_t* q) { return *reinterpret_cast<const uint4*>(q); };
   f32x4_t acc[T];
@@ -89,58 +88,63 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
   const int full = (int)(p.k >> 7);  // whole blocks
   const int b0 = (int)((int64_t)full * w / waves), b1 = (int)((int64_t)full * (w + 1) / waves);
 
+  struct Blocks {
+    uint4 w[U][NT][2], x[U][MT][2];
+  };
   // Past the share's end: the last block again (with factor zero).
-  const auto load_w = [&](int b, uint4 (&a)[U][NT][2]) {
+  const auto fetch = [&](int b, Blocks& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t o = 128 * (int64_t)(b + u < b1 ? b + u : b1 - 1);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) a[u][t][0] = load(wp[t] + o), a[u][t][1] = load(wp[t] + o + 64);
+      for (int t = 0; t < NT; ++t) v.w[u][t][0] = load(wp[t] + o), v.w[u][t][1] = load(wp[t] + o + 64);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) v.x[u][t][0] = load(xp[t] + o), v.x[u][t][1] = load(xp[t] + o + 64);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // Blocks b .. b + U with W in a.  X is loaded before the next blocks of W:
-  // loads return in order, and W's come from further away.
-  const auto step = [&](int b, const uint4 (&a)[U][NT][2], auto more, uint4 (&next)[U][NT][2]) {
-    uint4 x[U][MT][2];
-    float f[U][MT];
+  const auto step = [&](int b, const Blocks& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int bb = b + u < b1 ? b + u : b1 - 1;
-      const int64_t o = 128 * (int64_t)bb;
-      const float sw = wsp[bb] * (b + u < b1 ? 1.0f : 0.0f);
+      const float live = b + u < b1 ? 1.0f : 0.0f, sw = wsp[bb] * live, sw2 = wsp2[bb] * live;
+      float f[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        x[u][t][0] = load(xp[t] + o), x[u][t][1] = load(xp[t] + o + 64);
-        f[u][t] = sx(t, bb) * sw;
-      }
-    }
-    if constexpr (decltype(more)::value) {
-      __builtin_amdgcn_sched_barrier(0);
-      load_w(b + U, next);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int t = 0; t < MT; ++t) f[t] = sx(t, bb);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const f32x4_t d = mfma128(a[u][t / MT][0], a[u][t / MT][1], x[u][t % MT][0], x[u][t % MT][1]);
+        const float ft = f[t % MT] * (16 * (t / MT) + 4 * g < rest ? sw : sw2);
+        const f32x4_t d = mfma128(v.w[u][t / MT][0], v.w[u][t / MT][1], v.x[u][t % MT][0], v.x[u][t % MT][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], f[u][t % MT], acc[t][e]);
+        for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], ft, acc[t][e]);
       }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
+  Blocks va, vb;
+  if (b0 < b1) fetch(b0, va);
+  if constexpr (SXL) {
+    for (int i = threadIdx.x; i < 16 * MT * p.kb; i += blockDim.x) {
+      const int rr = i / p.kb, c = i - rr * p.kb;
+      const int64_t xi = i0 + rr < rows.count ? i0 + rr : rows.count - 1;
+      sxl[rr * ld + c] = p.xs[rows.x_row(xi) * p.kb + c];
+    }
+    __syncthreads();
+  }
   if (b0 < b1) {
-    uint4 wa[U][NT][2], wb[U][NT][2];
-    load_w(b0, wa);
     int b = b0;
     for (; b + 2 * U < b1; b += 2 * U) {
-      step(b, wa, std::true_type(), wb);
-      step(b + U, wb, std::true_type(), wa);
+      fetch(b + U, vb);
+      step(b, va);
+      fetch(b + 2 * U, va);
+      step(b + U, vb);
     }
     if (b + U < b1) {
-      step(b, wa, std::true_type(), wb);
-      step(b + U, wb, std::false_type(), wa);
+      fetch(b + U, vb);
+      step(b, va);
+      step(b + U, vb);
     } else {
-      step(b, wa, std::false_type(), wb);
+      step(b, va);
     }
   }
   if (full < p.kb && w == waves - 1) {
@@ -148,26 +152,26 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
     const int64_t k0 = 128 * (int64_t)full, end = p.k - 16 - 16 * g;
     const bool in0 = k0 <= end, in1 = k0 + 64 <= end;
     const int64_t o0 = in0 ? k0 : end, o1 = in1 ? k0 + 64 : end;
-    const float sw = wsp[full];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const uint8_t* xt = xp[t % MT];
       const uint4 z = make_uint4(0, 0, 0, 0), x0 = load(xt + o0), x1 = load(xt + o1);
       const f32x4_t d = mfma128(load(wp[t / MT] + o0), load(wp[t / MT] + o1), in0 ? x0 : z, in1 ? x1 : z);
-      const float f = sx(t % MT, full) * sw;
+      const float f = sx(t % MT, full) * (16 * (t / MT) + 4 * g < rest ? wsp : wsp2)[full];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], f, acc[t][e]);
     }
   }
   // The sums of GT blocks at a time (what LDS holds of all wavefronts).
-  constexpr int GT = T < 4 ? T : 4;
+  constexpr int GT = sums_at_a_time(T);
 #pragma unroll
   for (int t0 = 0; t0 < T; t0 += GT) {
     if (t0 > 0) __syncthreads();
 #pragma unroll
-    for (int t = 0; t < GT; ++t) red[(w * GT + t) * 64 + lane] = acc[t0 + t];
+    for (int t = 0; t < GT; ++t)
+      if (t0 + t < T) red[(w * GT + t) * 64 + lane] = acc[t0 + t < T ? t0 + t : 0];
     __syncthreads();
-    for (int tt = w; tt < GT; tt += waves) {
+    for (int tt = w; tt < GT && t0 + tt < T; tt += waves) {
       const int t = t0 + tt;
       f32x4_t sum = red[tt * 64 + lane];
       for (int i = 1; i < waves; ++i) {
@@ -177,7 +181,7 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
       }
       // Item e of lane (r, g): weight row 4 g + e, activation row r.
       const int64_t i = i0 + 16 * (t % MT) + r, col = n0 + 16 * (t / MT) + 4 * g;
-      if (i >= rows.count || col >= p.n) continue;
+      if (i >= rows.count || col >= n1) continue;
       uint16_t* dst = p.y + rows.out_row(i) * p.n + col;
       if ((p.n & 3) == 0) {
         const bf16x2_t lo = {(__bf16)sum[0], (__bf16)sum[1]}, hi = {(__bf16)sum[2], (__bf16)sum[3]};
@@ -186,7 +190,7 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + e < p.n) dst[e] = (uint16_t)f32_to_bf16_rne(sum[e]);
+          if (col + e < n1) dst[e] = (uint16_t)f32_to_bf16_rne(sum[e]);
       }
     }
   }
@@ -194,10 +198,10 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
 
 template <int MT, int NT, int U, int MAXW, bool SXL>
 __global__ void __launch_bounds__(64 * MAXW) fp8_skinny_kernel(SkinnyArgs p) {
-  __shared__ f32x4_t red[MAXW * (MT * NT < 4 ? MT * NT : 4) * 64];
+  __shared__ f32x4_t red[MAXW * sums_at_a_time(MT * NT) * 64];
   extern __shared__ float sxl[];
   const int64_t i0 = (int64_t)blockIdx.y * (16 * MT);
-  skinny_tile<MT, NT, U, SXL>(p, p.wq, p.ws, (int64_t)blockIdx.x * (16 * NT), RowSpan{p.m, nullptr, 1}, i0,
+  skinny_tile<MT, NT, U, SXL>(p, p.wq, p.ws, (int64_t)blockIdx.x * p.span, RowSpan{p.m, nullptr, 1}, i0,
                          blockDim.x >> 6, red, sxl);
 }
 
@@ -210,7 +214,7 @@ constexpr int kMaxPairs = 1024;
 
 template <int MT, int NT, int U, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
-  __shared__ f32x4_t red[WAVES * (MT * NT < 4 ? MT * NT : 4) * 64];
+  __shared__ f32x4_t red[WAVES * sums_at_a_time(MT * NT) * 64];
   __shared__ int32_t same[kMaxPairs];
   __shared__ int32_t count, earlier;
   const int pair = blockIdx.y, pairs = (int)p.m;
@@ -239,15 +243,51 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
 
 }  // namespace
 
-// Few rows: the weight streams through registers.  From 33 rows on the reads of X
-// cost more than the GEMM's tiles, unless the weight is small (64 rows of X,
-// skinny against GEMM: 17408 x 5120 51.7 / 45.5 us, 5120 x 17408 77 / 38 us, 5120
-// x 5120 20 / 20 us, 1024 x 2048 7.3 us against two launches of 5).
-static bool use_gemm(int64_t m, int64_t n, int64_t k) {
-  return m > 32 && (m > 64 || n > ((int64_t)1 << 25) / k) && fp8_gemm_supported(m, n, k);
+namespace {
+
+constexpr int kCus = 256, kMaxSpan = 80;
+constexpr size_t kScalesLds = 65536;
+
+// Few rows: each CU streams its share of W through registers and reads all of X,
+// and the sum of both bounds it.  A CU takes 43 ns per KB from HBM (6.1 TB/s over
+// the chip; a CU by itself is no faster, so shares have to be even) and 31 ns per
+// KB of X from L2, the lines in flight being what is scarce; 4 us pass before and
+// after.  17408 x 5120 with M = 1, 16, 32, 48: 19.0, 21.2, 24.6 and 28.4 us.
+struct Skinny {
+  int mt = 1;        // 16 mt rows of X per workgroup
+  int64_t span = 0;  // rows of W per workgroup; 0: scales too long for LDS
+  int64_t rounds = 1;
+  double ns = 0;
+};
+
+// The rows of W in even shares, multiples of 4, of one workgroup per CU, or of as
+// many rounds of them as spans of at most 80 need.
+Skinny skinny_plan(int64_t m, int64_t n, int64_t k) {
+  Skinny p;
+  const int64_t kb = (k + 127) / 128, fit = (int64_t)(kScalesLds / 64) / (kb | 1);
+  int64_t gy = (m + 63) / 64;
+  p.mt = (int)(((m + 15) / 16 + gy - 1) / gy);
+  if (p.mt > fit) p.mt = fit < 1 ? 1 : (int)fit;
+  gy = (m + 16 * p.mt - 1) / (16 * p.mt);
+  const int64_t cols = kCus / gy > 0 ? kCus / gy : 1;
+  p.rounds = (n + cols * kMaxSpan - 1) / (cols * kMaxSpan);
+  int64_t span = (n + cols * p.rounds - 1) / (cols * p.rounds);
+  span = (span + 3) / 4 * 4;
+  const double wgs = (double)((n + span - 1) / span) * (double)gy;
+  p.ns = 4000.0 + (wgs > kCus ? wgs / kCus : 1.0) * (43.0 * (double)span + 31.0 * 16 * p.mt) * (double)k / 1024;
+  if (fit >= 1) p.span = span;
+  return p;
 }
 
-// Otherwise 16 or 32 rows of W per workgroup along x, at least 16 of X along y.
+}  // namespace
+
+// Measured, skinny against GEMM, us: M = 48 17408 x 5120 28.4 / 38.8, 5120 x 17408
+// 43.5 / 26.6; M = 96 5120 x 5120 21.8 / 18.1, 1024 x 2048 8.1 / 10.5.
+static bool use_gemm(int64_t m, int64_t n, int64_t k) {
+  return m > 16 && fp8_gemm_supported(m, n, k) && fp8_gemm_ns(m, n, k) < skinny_plan(m, n, k).ns;
+}
+
+// Otherwise at least 4 rows of W per workgroup along x, at least 16 of X along y.
 bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) || (n <= ((int64_t)1 << 26) && m <= 16 * 65535 && k <= ((int64_t)1 << 37));
 }
@@ -256,7 +296,7 @@ int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
 }
 
-// The GEMM's tiles: 128 pairs each, the last of an expert with fewer.
+// Few pairs, and few per expert.
 static bool use_routed(int64_t pairs, int64_t experts, int64_t n) {
   return pairs <= kMaxPairs && pairs <= 16 * experts && n <= ((int64_t)1 << 26);
 }
@@ -268,32 +308,42 @@ bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64
 }
 
 // As few wavefronts as keep the number of passes over U blocks that MAXW allow.
-template <int MT, int NT, int U, int MAXW>
+template <int MT, int NT, int U, int MAXW, bool SXL = true>
 static void launch_skinny_shape(const SkinnyArgs& a, hipStream_t s) {
   const int passes = (a.kb + MAXW * U - 1) / (MAXW * U), waves = (a.kb + passes * U - 1) / (passes * U);
-  const dim3 grid((unsigned)((a.n + 16 * NT - 1) / (16 * NT)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT)));
-  const size_t lds = sizeof(float) * 16 * MT * (a.kb | 1);
-  if (lds <= 16384) fp8_skinny_kernel<MT, NT, U, MAXW, true><<<grid, 64 * waves, lds, s>>>(a);
-  else fp8_skinny_kernel<MT, NT, U, MAXW, false><<<grid, 64 * waves, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.n + a.span - 1) / a.span), (unsigned)((a.m + 16 * MT - 1) / (16 * MT)));
+  const size_t lds = SXL ? sizeof(float) * 16 * MT * (a.kb | 1) : 0;
+  fp8_skinny_kernel<MT, NT, U, MAXW, SXL><<<grid, 64 * waves, lds, s>>>(a);
+}
+
+// Blocks of W in flight: about 8 to 10 KB per wavefront and buffer.  Eight
+// wavefronts, or four where two workgroups are to share a CU (34816 x 5120, M = 1
+// / 32: 34.8 / 44.1 us against 37.2 / 46.6) or eight would not leave the registers
+// (MT = 4, NT = 5).
+template <int MT>
+static void launch_skinny(const SkinnyArgs& a, int64_t rounds, hipStream_t s) {
+  if (a.span <= 16) return launch_skinny_shape<MT, 1, 4 - MT / 2, 8>(a, s);
+  if (a.span <= 32) return launch_skinny_shape<MT, 2, MT <= 2 ? 2 : 1, 8>(a, s);
+  if (a.span <= 48) return launch_skinny_shape<MT, 3, 1, 8>(a, s);
+  if constexpr (MT < 4)
+    if (rounds == 1) return launch_skinny_shape<MT, 5, 1, 8>(a, s);
+  launch_skinny_shape<MT, 5, 1, 4>(a, s);
 }
 
 void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                        const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
-  const SkinnyArgs a{xq, xs, wq, ws, y, m, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), nullptr, 1, 1};
   if (use_gemm(m, n, k)) return launch_fp8_gemm(xq, xs, m, n, k, wq, ws, y, workspace, s);
-  // Per shape: us at K = 5120 (N = 17408) / K = 17408 (N = 5120) / N = 1024, K = 2048.
-  if (m <= 16) {
-    // Two rows of blocks a wavefront read X half as often; few rows of W need
-    // every workgroup they can make.  M = 8: 24.2 / 26.3 / 5.6 against 28.6 / 33.2 / 4.5.
-    if (n > 2048) launch_skinny_shape<1, 2, 2, 4>(a, s);
-    else launch_skinny_shape<1, 1, 4, 8>(a, s);
-  } else if (m <= 32) {
-    // M = 32: 34.6 / 43.1 / 6.9, 36.2 / 37.0 / 7.1 and 41.1 / 54.0 / 6.1.
-    if (n <= 2048) launch_skinny_shape<2, 1, 2, 4>(a, s);
-    else if (k <= 8192) launch_skinny_shape<2, 2, 1, 8>(a, s);
-    else launch_skinny_shape<2, 2, 2, 4>(a, s);
-  } else {
-    launch_skinny_shape<2, 2, 1, 4>(a, s);
+  const Skinny p = skinny_plan(m, n, k);
+  SkinnyArgs a{xq, xs, wq, ws, y, m, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), (int)p.span, nullptr, 1, 1};
+  if (p.span == 0) {
+    a.span = 32;
+    return launch_skinny_shape<1, 2, 2, 4, false>(a, s);
+  }
+  switch (p.mt) {
+    case 1: return launch_skinny<1>(a, p.rounds, s);
+    case 2: return launch_skinny<2>(a, p.rounds, s);
+    case 3: return launch_skinny<3>(a, p.rounds, s);
+    default: return launch_skinny<4>(a, p.rounds, s);
   }
 }
 
@@ -302,7 +352,7 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
                                void* workspace, hipStream_t s) {
   const int64_t pairs = t_count * topk;
   if (use_routed(pairs, experts, n)) {
-    const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), route, experts,
+    const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), 32, route, experts,
                        topk};
     const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pairs);
     fp8_routed_kernel<1, 2, 2, 4><<<grid, 256, 0, s>>>(a);

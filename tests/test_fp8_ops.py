@@ -377,6 +377,29 @@ def test_fp8_linear_large_exact(nv, m, n, k):
         assert not bool(bad.any()), f"workspace {ws}: {int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
 
 
+# Up to 64 rows: shares of 4, 20, 36, 52 (and 48, 56, 68 in more rounds) rows of W, which cross the blocks of 128 anywhere.
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 17, 34, 64])
+@pytest.mark.parametrize("n,k", [(1000, 272), (5000, 1040), (9003, 272), (13000, 400), (21000, 144), (28001, 256), (34816, 128)])
+def test_fp8_linear_shares_exact(nv, m, n, k):
+    xq, xs, wq, ws = exact_operands(m, n, k, 900 + m + n + k)
+    y = torch.full((m + 1, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    nv.fp8_linear(*map(dev, (xq, xs, wq, ws)), out=y[:m])
+    ref, bound = (np.concatenate(v, axis=1) for v in zip(*(
+        F.linear(xq, xs, wq[i:i + 1024], ws[i // 128:i // 128 + 8]) for i in range(0, n, 1024))))
+    check_exact(y[:m], ref, bound)
+    assert (y[m] == 7.0).all()
+
+
+# Scales of X that fit LDS for fewer rows at a time, or not at all.
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(17, 20, 70000), (60, 9, 33008), (3, 33, 131200), (18, 5, 262160)])
+def test_fp8_linear_long_rows(nv, m, n, k):
+    xq, xs, wq, ws = operands(m, n, k, 950 + m)
+    y = nv.fp8_linear(*map(dev, (xq, xs, wq, ws)))
+    check(y, *F.linear(xq, xs, wq, ws), k)
+
+
 @pytest.mark.gpu
 def test_fp8_linear_takes_float8_tensors(nv):
     xq, xs, wq, ws = (dev(a) for a in operands(3, 40, 144, 600))
