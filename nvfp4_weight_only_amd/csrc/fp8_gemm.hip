@@ -134,12 +134,16 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   // Workgroups go to the 8 XCDs round-robin by id; when the count allows,
   // consecutive ids of one XCD take all m tiles of consecutive n tiles, so a
   // tile's rows of W are fetched into that XCD's L2 once.
-  const int tiles = p.n_tiles * p.m_tiles;
-  int id = (int)blockIdx.x;
-  const int slice = id / tiles;
-  id -= slice * tiles;
-  if ((tiles & 7) == 0) id = (id & 7) * (tiles >> 3) + (id >> 3);
-  const int nt = id / p.m_tiles, mt = id % p.m_tiles;
+  int id = (int)blockIdx.x, slice = 0, nt, mt;
+  if constexpr (GROUPED) {
+    nt = (id >> 3) % p.n_tiles, mt = (id >> 3) / p.n_tiles;
+  } else {
+    const int tiles = p.n_tiles * p.m_tiles;
+    slice = id / tiles;
+    id -= slice * tiles;
+    if ((tiles & 7) == 0) id = (id & 7) * (tiles >> 3) + (id >> 3);
+    nt = id / p.m_tiles, mt = id % p.m_tiles;
+  }
   const int64_t n0 = (int64_t)nt * TN;
   const uint8_t* wq = p.wq;
   const float* ws = p.ws;
@@ -149,13 +153,17 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     const int32_t* pair_off = p.groups + p.experts;
     const int32_t* tile_off = p.groups + 2 * p.experts + 1;
     perm = p.groups + 3 * p.experts + 2;
-    const int used = tile_off[p.experts];
-    if (mt >= used) {  // zero rows for the pairs whose id is out of range
-      const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN;
-      for (int64_t i = (int64_t)pair_off[p.experts] + mt - used; i < p.m; i += p.m_tiles - used)
+    // Each XCD takes an eighth of the tiles in use, all of their n tiles, so that
+    // the rows of X too are fetched into its L2 once.  The workgroups left over
+    // write zero rows for the pairs whose id is out of range.
+    const int64_t used = tile_off[p.experts], xcd = id & 7, t0 = used * xcd >> 3, tn = (used * (xcd + 1) >> 3) - t0;
+    if (mt >= tn) {
+      const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN, left = 8 * (int64_t)p.m_tiles - used;
+      for (int64_t i = pair_off[p.experts] + xcd * p.m_tiles - t0 + mt - tn; i < p.m; i += left)
         for (int64_t c = tid; c < cols; c += 512) p.y[perm[i] * p.ld + n0 + c] = 0;
       return;
     }
+    mt += (int)t0;
     int64_t lo = 0, hi = p.experts - 1;  // the expert with tile_off[e] <= mt < tile_off[e + 1]
     while (lo < hi) {
       const int64_t mid = (lo + hi + 1) >> 1;
@@ -512,7 +520,7 @@ int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
   const int64_t pairs = t_count * topk, kb = (k + kChunk - 1) / kChunk;
   return k <= ((int64_t)1 << 23) && t_count <= ((int64_t)UINT32_MAX) / k && t_count <= (int64_t)UINT32_MAX / 4 / kb &&
-         (pairs + 127) / 128 + experts <= ((int64_t)1 << 22) / ((n + 255) / 256);
+         (pairs + 127) / 128 + experts + 8 <= ((int64_t)1 << 22) / ((n + 255) / 256);
 }
 
 void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,
@@ -520,10 +528,11 @@ void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, c
                              hipStream_t s) {
   // Fewer than one tile past pairs / 128 for each expert that has pairs; at least
   // one workgroup is left for rows of zeros if there are any.
-  const int64_t m_tiles = (pairs + 127) / 128 + (experts < pairs ? experts : pairs), n_tiles = (n + 255) / 256;
+  const int64_t m_tiles = ((pairs + 127) / 128 + (experts < pairs ? experts : pairs) + 7) / 8;  // per XCD
+  const int64_t n_tiles = (n + 255) / 256;
   const GemmArgs a{xq, xs, wq, ws, y, pairs, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128),
                    (int)n_tiles, (int)m_tiles, 1, nullptr, groups, experts, topk};
-  fp8_gemm_kernel<256, 128, 4, 2, 3, true><<<dim3((unsigned)(n_tiles * m_tiles)), 512, 0, s>>>(a);
+  fp8_gemm_kernel<256, 128, 4, 2, 3, true><<<dim3((unsigned)(8 * n_tiles * m_tiles)), 512, 0, s>>>(a);
 }
 
 void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,

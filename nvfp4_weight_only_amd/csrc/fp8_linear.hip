@@ -355,7 +355,7 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
     const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), 32, route, experts,
                        topk};
     const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pairs);
-    fp8_routed_kernel<1, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+    fp8_routed_kernel<1, 2, 1, 4><<<grid, 256, 0, s>>>(a);
     return;
   }
   int32_t* groups = static_cast<int32_t*>(workspace);
