@@ -164,11 +164,13 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
       return;
     }
     mt += (int)t0;
-    int64_t lo = 0, hi = p.experts - 1;  // the expert with tile_off[e] <= mt < tile_off[e + 1]
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (tile_off[mid] <= mt) lo = mid;
-      else hi = mid - 1;
+    // The last expert with tile_off[e] <= mt: 64 candidates at a time.
+    int64_t lo = 0, len = p.experts;
+    while (len > 1) {
+      const int64_t step = (len + 63) >> 6, e = lo + step * lane;
+      const uint64_t in = __ballot(step * lane < len && tile_off[step * lane < len ? e : lo] <= mt);
+      const int64_t at = step * (63 - __builtin_clzll(in | 1));
+      lo += at, len = len - at < step ? len - at : step;
     }
     m0 = pair_off[lo] + (int64_t)(mt - tile_off[lo]) * TM;
     rows = pair_off[lo + 1] - m0 < TM ? pair_off[lo + 1] - m0 : TM;
