@@ -15,6 +15,8 @@
 // LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
 // piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
 // covers all banks.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -236,10 +238,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   const bool past = ktail != 0 && 16 * piece >= ktail;
   const uint32_t back = past ? (uint32_t)(16 * piece - (ktail - 16)) : 0u;
 
-  // Load q (of NL) of chunk c into stage s; past the end the last chunk again, so
-  // that every chunk leaves the same number of loads behind.
-  const auto issue = [&](int q, int c, int s) {
-    const int cc = c < last ? c : last;
+  // Load q (of NL) of chunk cc into stage s.
+  const auto issue = [&](int q, int cc, int s) {
     Stage<TN, TM>& sg = stage[s];
     const int64_t k0 = (int64_t)cc * kChunk;
     const uint32_t bk = cc == p.kb - 1 ? back : 0u;
@@ -291,11 +291,14 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   // everything of this chunk's stage has been read and the next chunk has
   // landed: after it the next chunk's fragments are read, and the chunk that
   // takes this stage is loaded, one load behind each matrix instruction.
+  constexpr int PART = QJ * MT < NL ? QJ * MT : NL;  // of a chunk's loads, those behind the last row of blocks
 #pragma unroll
   for (int s = 0; s < ST; ++s)
+    if (c0 + s <= last)
 #pragma unroll
-    for (int q = 0; q < NL; ++q) issue(q, c0 + s, s);
-  wait_loads<(ST - 1) * NL>();
+      for (int q = 0; q < (s < ST - 1 ? NL : PART); ++q) issue(q, c0 + s, s);
+  if (c0 + ST - 1 <= last) wait_loads<(ST - 2) * NL + PART>();
+  else wait_loads<0>();
   finish(c0, 0);
   meet();
   i32x8_t a[2], b[MT];
@@ -316,7 +319,9 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
 #pragma unroll
   for (int j = 0; j < MT; ++j) f[j] = 0.0f;
   int sidx = 0;
-  for (int c = c0; c < c1; ++c) {
+  // REST, NEXT: the rest of chunk c - 1 + ST, and the first loads of chunk c + ST, are there to be issued.
+  const auto step = [&](int c, auto rest, auto next) {
+    constexpr bool REST = decltype(rest)::value, NEXT = decltype(next)::value;
     const int here = sidx;
     sidx = sidx + 1 == ST ? 0 : sidx + 1;
     const uint32_t so = (uint32_t)(here * sizeof(Stage<TN, TM>)), sn = (uint32_t)(sidx * sizeof(Stage<TN, TM>));
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
       if (i < NT - 1) {
         a[(i + 1) & 1] = read(so + rw, i + 1);
       } else {
-        wait_loads<(ST - 2) * NL + L2>();
+        wait_loads<REST ? (ST - 2) * NL + L2 : 0>();
         finish(c + 1, sidx);
         meet();
         a[0] = read(sn + rw, 0);
@@ -346,10 +351,10 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
           b[j] = read(sn + rx, j);
           sx[j] = stage[sidx].sx[16 * wm * MT + l16 + 16 * j];
 #pragma unroll
-          for (int q = QJ * j; q < QJ * (j + 1) && q < NL; ++q) issue(q, c + ST, here);
+          for (int q = QJ * j; NEXT && q < QJ * (j + 1) && q < NL; ++q) issue(q, c + ST, here);
         } else {
 #pragma unroll
-          for (int q = QJ * (t + MT); q < QJ * (t + MT + 1) && q < NL; ++q)
+          for (int q = QJ * (t + MT); REST && q < QJ * (t + MT + 1) && q < NL; ++q)
             issue(q, c - 1 + ST, here == 0 ? ST - 1 : here - 1);
         }
         const float fu = t < 2 ? f_old[t] : f[u % MT];
@@ -359,12 +364,16 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-  }
+  };
+  int c = c0;
+  for (; c + ST <= last; ++c) step(c, std::true_type(), std::true_type());
+  if (c - 1 + ST <= last) step(c++, std::true_type(), std::false_type());
+  for (; c <= last; ++c) step(c, std::false_type(), std::false_type());
 #pragma unroll
   for (int u = T - 2; u < T; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[u][e] = __builtin_fmaf(d[u & 3][e], f[u % MT], acc[u][e]);
-  wait_loads<0>();  // the repeat loads past the end have landed
+  wait_loads<0>();
   __syncthreads();
 
   // Block t = i MT + j: lane (l16, g) holds row 16 j + l16 of X and rows 4 g +
