@@ -45,9 +45,10 @@ struct RowSpan {
   __device__ __forceinline__ int64_t x_row(int64_t i) const { return pairs ? (uint32_t)pairs[i] / topk : i; }
 };
 
-// 16 NT rows of W against 16 MT rows of X by a workgroup of `waves` wavefronts,
-// each of which takes a contiguous share of the whole blocks of K, U blocks at a
-// time, with the next U blocks of W already on their way; the last wavefront
+// `span` rows of W (up to 16 NT) against 16 MT rows of X by a workgroup of `waves`
+// wavefronts, each of which takes a contiguous share of the whole blocks of K, U
+// blocks of both operands at a time with the next U on their way (in registers:
+// nothing of W is used twice, and X by one wavefront only); the last wavefront
 // adds the last, short block.  Their sums meet in LDS and are added in wavefront
 // order.  SXL: the rows' scales are first copied to LDS.
 constexpr int sums_at_a_time(int t) { return t <= 10 ? t : (t + 1) / 2; }
@@ -65,8 +66,8 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
     const int64_t wr = n0 + 16 * t + r < n1 ? n0 + 16 * t + r : n1 - 1;
     wp[t] = wq + wr * p.k + 16 * g;
   }
-  // The rows of W lie in one block of 128 or two: quad 4 g of rows of W (the
-  // rows of this lane's results) in the second one from block t on.
+  // The rows of W lie in one block of 128 or two; four neighbouring ones, as a
+  // lane has them of each 16, in one (spans are multiples of 4).
   const float* wsp = ws + (n0 >> 7) * p.kb;
   const float* wsp2 = ws + ((n1 - 1) >> 7) * p.kb;
   const int rest = 128 - (int)(n0 & 127);
@@ -107,13 +108,13 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int bb = b + u < b1 ? b + u : b1 - 1;
-      const float live = b + u < b1 ? 1.0f : 0.0f, sw = wsp[bb] * live, sw2 = wsp2[bb] * live;
+      const float sw = wsp[bb], sw2 = wsp2[bb];
       float f[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) f[t] = sx(t, bb);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const float ft = f[t % MT] * (16 * (t / MT) + 4 * g < rest ? sw : sw2);
+        const float ft = b + u < b1 ? f[t % MT] * (16 * (t / MT) + 4 * g < rest ? sw : sw2) : 0.0f;
         const f32x4_t d = mfma128(v.w[u][t / MT][0], v.w[u][t / MT][1], v.x[u][t % MT][0], v.x[u][t % MT][1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], ft, acc[t][e]);
@@ -205,12 +206,14 @@ __global__ void __launch_bounds__(64 * MAXW) fp8_skinny_kernel(SkinnyArgs p) {
                          blockDim.x >> 6, red, sxl);
 }
 
-// Few pairs over an expert stack, without a sort: workgroup (x, p) multiplies 16
-// NT rows of W of pair p's expert with the activations of every pair that chose
+// Few pairs over an expert stack, without a sort: workgroup (x, p) multiplies
+// span rows of W of pair p's expert with the activations of every pair that chose
 // that expert, if p is the first of them (the others' workgroups end); a pair
 // whose id is out of range gets zeros.  The order in which the pairs are found
-// varies; every output depends on its own rows only.
-constexpr int kMaxPairs = 1024;
+// varies; every output depends on its own rows only.  HBM bounds it: 8 tokens, top
+// 8 of 128, 2048 x 4096: 410 MB in 70 us, 5.9 TB/s (81 us with two blocks of K at a
+// time and the registers for two workgroups per CU instead of four).
+constexpr int kMaxPairs = 512;
 
 template <int MT, int NT, int U, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
@@ -248,7 +251,7 @@ namespace {
 constexpr int kCus = 256, kMaxSpan = 80;
 constexpr size_t kScalesLds = 65536;
 
-// Few rows: each CU streams its share of W through registers and reads all of X,
+// Few rows of X: each CU streams its share of W through registers and reads all of X,
 // and the sum of both bounds it.  A CU takes 43 ns per KB from HBM (6.1 TB/s over
 // the chip; a CU by itself is no faster, so shares have to be even) and 31 ns per
 // KB of X from L2, the lines in flight being what is scarce; 4 us pass before and
@@ -296,9 +299,13 @@ int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
 }
 
-// Few pairs, and few per expert.
+// Few pairs, and few per expert; of very few, more per expert, where the GEMM
+// has few tiles.  us, this against sort and GEMM: 128 experts 2048 x 4096 with 1,
+// 4, 8 pairs per expert 112 / 136, 201 / 198, 264 / 202; 16 of 4096 x 4096 with 4,
+// 6 50.9 / 49.3, 55.0 / 49.8; 8 of 14336 x 4096 with 8 96 / 120; 256 of 512 x 2048
+// with 2, 4 48.9 / 49.7, 68 / 56.
 static bool use_routed(int64_t pairs, int64_t experts, int64_t n) {
-  return pairs <= kMaxPairs && pairs <= 16 * experts && n <= ((int64_t)1 << 26);
+  return pairs <= kMaxPairs && pairs <= (pairs <= 64 ? 8 : 4) * experts && n <= ((int64_t)1 << 26);
 }
 
 bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {

@@ -1,5 +1,6 @@
 """The E4M3 operators with block scales: refusals of the C entry points and the binding (CPU), and the HIP kernels
 against the float64 oracle (GPU)."""
+import math
 import os
 
 import numpy as np
@@ -426,6 +427,25 @@ def test_fp8_linear_nan_and_zero(nv, m):
     ok = ~nan
     ok[2] = False
     assert np.all(np.abs(y - ref)[ok] <= F.linear_tolerance(ref, bound, k)[ok])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [640, 1040])
+@pytest.mark.parametrize("m", [1, 20, 40, 64, 300])
+def test_fp8_linear_infinite_scales(nv, m, k):
+    """A block's sum times its scale: an infinite scale gives an infinity, not NaN, in its rows or columns alone."""
+    n = 300
+    xq, wq = torch.full((m, k), 0x38, dtype=torch.uint8), torch.full((n, k), 0x38, dtype=torch.uint8)   # 1.0
+    xs, ws = torch.full((m, -(-k // 128)), 0.5), torch.full((3, -(-k // 128)), 2.0)
+    want = torch.full((m, n), float(k)).bfloat16()
+    ws[1, 4] = math.inf
+    want[:, 128:256] = math.inf
+    xs[m - 1, 2] = math.inf
+    want[m - 1] = math.inf
+    args = [a.cuda() for a in (xq, xs, wq, ws)]
+    assert torch.equal(nv.fp8_linear(*args).cpu(), want)
+    route = torch.zeros((m, 1), dtype=torch.int32, device="cuda")
+    assert torch.equal(nv.fp8_linear_grouped(*args[:2], route, args[2][None], args[3][None]).cpu()[:, 0], want)
 
 
 def routing(kind, t, topk, e, seed):
