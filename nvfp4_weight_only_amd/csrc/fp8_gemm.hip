@@ -523,7 +523,7 @@ bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) {
   return k <= ((int64_t)1 << 23) && (m + 63) / 64 <= ((int64_t)1 << 22) / ((n + 127) / 128);
 }
 
-double fp8_gemm_ns(int64_t m, int64_t n, int64_t k) { return gemm_plan(m, n, k, true).ns; }
+double fp8_gemm_ns(int64_t m, int64_t n, int64_t k, bool split) { return gemm_plan(m, n, k, split).ns; }
 
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = gemm_plan(m, n, k, true);

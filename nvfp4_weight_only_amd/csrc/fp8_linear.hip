@@ -282,21 +282,27 @@ Skinny skinny_plan(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
+// At least 4 rows of W per workgroup along x, at least 16 of X along y.
+bool skinny_supported(int64_t m, int64_t n, int64_t k) {
+  return n <= ((int64_t)1 << 26) && m <= 16 * 65535 && k <= ((int64_t)1 << 37);
+}
+
 }  // namespace
 
 // Measured, skinny against GEMM, us: M = 48 17408 x 5120 28.4 / 38.8, 5120 x 17408
 // 43.5 / 26.6; M = 96 5120 x 5120 21.8 / 18.1, 1024 x 2048 8.1 / 10.5.
-static bool use_gemm(int64_t m, int64_t n, int64_t k) {
-  return m > 16 && fp8_gemm_supported(m, n, k) && fp8_gemm_ns(m, n, k) < skinny_plan(m, n, k).ns;
+// `split`: whether there is a workspace to split K with.
+static bool use_gemm(int64_t m, int64_t n, int64_t k, bool split) {
+  if (!skinny_supported(m, n, k)) return true;
+  return m > 16 && fp8_gemm_supported(m, n, k) && fp8_gemm_ns(m, n, k, split) < skinny_plan(m, n, k).ns;
 }
 
-// Otherwise at least 4 rows of W per workgroup along x, at least 16 of X along y.
 bool fp8_linear_supported(int64_t m, int64_t n, int64_t k) {
-  return use_gemm(m, n, k) || (n <= ((int64_t)1 << 26) && m <= 16 * 65535 && k <= ((int64_t)1 << 37));
+  return skinny_supported(m, n, k) || fp8_gemm_supported(m, n, k);
 }
 
 int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  return use_gemm(m, n, k) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
+  return use_gemm(m, n, k, true) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
 }
 
 // Few pairs, and few per expert; of very few, more per expert, where the GEMM
@@ -339,7 +345,7 @@ static void launch_skinny(const SkinnyArgs& a, int64_t rounds, hipStream_t s) {
 
 void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                        const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
-  if (use_gemm(m, n, k)) return launch_fp8_gemm(xq, xs, m, n, k, wq, ws, y, workspace, s);
+  if (use_gemm(m, n, k, workspace != nullptr)) return launch_fp8_gemm(xq, xs, m, n, k, wq, ws, y, workspace, s);
   const Skinny p = skinny_plan(m, n, k);
   SkinnyArgs a{xq, xs, wq, ws, y, m, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), (int)p.span, nullptr, 1, 1};
   if (p.span == 0) {

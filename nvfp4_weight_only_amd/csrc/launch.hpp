@@ -154,7 +154,7 @@ int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
 void launch_fp8_linear(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                        const float* ws, uint16_t* y, void* workspace, hipStream_t s);
 bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k);
-double fp8_gemm_ns(int64_t m, int64_t n, int64_t k);  // estimated time
+double fp8_gemm_ns(int64_t m, int64_t n, int64_t k, bool split);  // estimated time
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k);
 void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                      const float* ws, uint16_t* y, void* workspace, hipStream_t s);
