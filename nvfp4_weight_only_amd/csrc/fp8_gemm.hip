@@ -5,12 +5,16 @@
 // TM rows of X).  K advances in chunks of 128, one scale block each: both
 // operands' chunk goes to LDS by direct loads (16 bytes per lane, whole
 // 128-byte lines per row) into a ring of ST stages, so that up to ST - 1 chunks
-// are in flight behind the one in use.  Per chunk a wavefront holds its rows of
-// X in registers, passes over its rows of W 32 at a time, and each 32 x 32
-// block of outputs takes two 32x32x64 matrix instructions (the first with C =
-// 0) and 16 fused multiply-adds that scale the block's sum into the FP32
-// accumulators.  The multiply-adds of one block are issued behind the next
-// block's matrix instructions, which run meanwhile.
+// are in flight behind the one in use.  A 16 x 16 block of outputs takes one
+// 16x16x128 matrix instruction per chunk (C = 0) and four fused multiply-adds per
+// lane that scale the block's sum into the FP32 accumulators; those of one block
+// are issued two blocks later, while the matrix instructions run on.
+//
+// What bounds it: 2048 x 17408 x 5120 takes 190 us, 1.9 PFLOP/s (177 us if every
+// load found its line in L2; the matrix instructions and multiply-adds by
+// themselves 115 us, the LDS reads, 192 KB per chunk of 64 KB, 90 us); 4096^3 68 us,
+// 2.0 PFLOP/s.  With few rows of X the loads: 333 x 5000 x 17392 66 us, 58 if they
+// found their lines in L2; 64 x 5120 x 17408 30 us, 3.0 TB/s of W.
 //
 // LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
 // piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
@@ -29,7 +33,8 @@ typedef __attribute__((address_space(3))) const void lds_t;
 constexpr int kChunk = 128;
 // Tiles with two stages only: how many chunks ahead of the loads to LDS lines are
 // brought into L2 (256 x 256 over 2048 x 16384 x 5120: 174 us without, 170 with;
-// deeper rings lose 5 to 15 % by it).
+// with three stages the lines come early enough, and the lines in flight are what
+// is scarce: 64 x 5120 x 17408 30 us without, 38 with).
 constexpr int kAhead = 2;
 
 struct GemmArgs {
@@ -158,7 +163,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     const int32_t* tile_off = p.groups + 2 * p.experts + 1;
     perm = p.groups + 3 * p.experts + 2;
     // Each XCD takes an eighth of the tiles in use, all of their n tiles, so that
-    // the rows of X too are fetched into its L2 once.  The workgroups left over
+    // the rows of X too are fetched into its L2 once (2048 x 4096, 256 tokens, top 8
+    // of 128: 213 us so, 277 by n tile).  The workgroups left over
     // write zero rows for the pairs whose id is out of range.
     const int64_t used = tile_off[p.experts], xcd = id & 7, t0 = used * xcd >> 3, tn = (used * (xcd + 1) >> 3) - t0;
     if (mt >= tn) {
@@ -420,7 +426,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   }
 }
 
-// Sums of the slices in slice order, 4 outputs per thread.
+// Sums of the slices in slice order, 4 outputs per thread: bound by its reads (4
+// slices of 333 x 5000: 5.6 us with the launch).
 __global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__ part, int slices, int64_t quads,
                                                        uint16_t* __restrict__ y) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -438,9 +445,9 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__
 
 namespace {
 
-// Tile shapes.  Measured per chunk of 128 and per tile (first loads and
-// epilogue), in ns, with a CU's slots filled: 256 x 256 at 1.9 PFLOP/s over the
-// chip, the smaller ones less (more LDS reads per product), but with finer
+// Tile shapes: ns per chunk of 128 and per tile (first loads and epilogue), as
+// measured with a CU's slots filled.  256 x 256 reaches 1.9 PFLOP/s over the chip,
+// the smaller ones less (more LDS reads and loads per product), but they have finer
 // steps for sizes that leave CUs idle.
 struct Shape {
   int tn, tm, per_cu;
@@ -485,7 +492,7 @@ Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
                     m * n > ((int64_t)1 << 26) / s))
         break;
       const double ns = shape_ns(kShapes[i], m, tiles * s, (chunks + s - 1) / s) +
-                        (s > 1 ? 1500.0 + 8.0 * (double)(m * n) * s / 4000.0 : 0.0);
+                        (s > 1 ? 2500.0 + 4.0 * (double)(m * n) * s / 4000.0 : 0.0);
       if (ns < best.ns) best = Plan{ns, i, s, 0};
     }
   }
