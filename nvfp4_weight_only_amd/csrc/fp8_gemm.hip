@@ -373,10 +373,29 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
       }
     }
   };
-  int c = c0;
-  for (; c + ST <= last; ++c) step(c, std::true_type(), std::true_type());
-  if (c - 1 + ST <= last) step(c++, std::true_type(), std::false_type());
-  for (; c <= last; ++c) step(c, std::false_type(), std::false_type());
+  // GROUPED: a wavefront whose rows of X are all past the tile's (its partner on the
+  // SIMD has the matrix cores for itself) loads and waits with the others (2048
+  // tokens, top 8 of 128: 301 us without, 289 with; 256 tokens: 210, 203).
+  const auto idle = [&](int c, auto rest, auto next) {
+    constexpr bool REST = decltype(rest)::value, NEXT = decltype(next)::value;
+    const int here = sidx;
+    sidx = sidx + 1 == ST ? 0 : sidx + 1;
+#pragma unroll
+    for (int q = PART; REST && q < NL; ++q) issue(q, c - 1 + ST, here == 0 ? ST - 1 : here - 1);
+    wait_loads<REST ? (ST - 2) * NL + L2 : 0>();
+    finish(c + 1, sidx);
+    meet();
+#pragma unroll
+    for (int q = 0; NEXT && q < PART; ++q) issue(q, c + ST, here);
+  };
+  const auto run = [&](const auto& f) {
+    int c = c0;
+    for (; c + ST <= last; ++c) f(c, std::true_type(), std::true_type());
+    if (c - 1 + ST <= last) f(c++, std::true_type(), std::false_type());
+    for (; c <= last; ++c) f(c, std::false_type(), std::false_type());
+  };
+  if (GROUPED && 16 * wm * MT >= rows) run(idle);
+  else run(step);
 #pragma unroll
   for (int u = T - 2; u < T; ++u)
 #pragma unroll
