@@ -378,6 +378,22 @@ def test_fp8_linear_large_exact(nv, m, n, k):
         assert not bool(bad.any()), f"workspace {ws}: {int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
 
 
+# Every tile of the GEMM with fewer chunks of K than its ring holds, as many, and more.
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(1500, 9000, 128), (4100, 2050, 256), (2048, 9000, 272), (2048, 9000, 384),
+                                   (260, 17408, 256), (200, 17408, 384), (260, 9000, 384), (2048, 700, 512),
+                                   (130, 17408, 2064), (4100, 260, 2064), (200, 9000, 2064)])
+def test_fp8_linear_few_chunks_exact(nv, m, n, k):
+    d = [dev(a) for a in exact_operands(m, n, k, 750 + m + n + k)]
+    x, w = decoded(d[0], d[1], 1), decoded(d[2], d[3], 128)
+    assert float((x.abs() @ w.abs().T).max()) < 2.0 ** 16
+    y = torch.full((m + 1, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    nv.fp8_linear(*d, out=y[:m])
+    bad = y[:m] != (x @ w.T).bfloat16()
+    assert not bool(bad.any()), f"{int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
+    assert bool((y[m] == 7).all())
+
+
 # Up to 64 rows: shares of 4, 20, 36, 52 (and 48, 56, 68 in more rounds) rows of W, which cross the blocks of 128 anywhere.
 @pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 17, 34, 64])
@@ -468,6 +484,23 @@ GROUPED_CASES = [(1, 1, 1, 16, 128, "uniform"), (1, 8, 128, 64, 256, "uniform"),
                  (3, 2, 5, 33, 1040, "none"), (20, 4, 6, 300, 272, "skew"), (130, 2, 3, 64, 512, "one"),
                  (200, 8, 16, 545, 256, "skew"), (300, 4, 6, 300, 1040, "uniform"), (40, 3, 700, 24, 144, "uniform"),
                  (4200, 8, 4, 16, 128, "uniform")]
+
+
+# Exact sums: without a sort, of one expert more pairs than the 16 of a pass; behind the sort, tiles of 128 pairs with
+# few rows, more than half and all of them, ids out of range.
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,topk,e,n,k,kind", [
+    (32, 1, 8, 100, 272, "one"), (64, 1, 8, 259, 400, "skew"), (64, 8, 128, 64, 256, "skew"), (128, 4, 200, 33, 144, "none"),
+    (256, 4, 8, 515, 272, "uniform"), (129, 4, 3, 260, 1040, "one"), (700, 2, 9, 1000, 400, "skew"),
+    (180, 3, 40, 257, 128, "none"), (2050, 1, 16, 300, 384, "uniform")])
+def test_fp8_linear_grouped_exact(nv, t, topk, e, n, k, kind):
+    xq, xs, wq, ws = exact_operands(t, n, k, 1000 + t + n + k, e)
+    route = routing(kind, t, topk, e, 1100 + t)
+    y = torch.full((t + 1, topk, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    nv.fp8_linear_grouped(*map(dev, (xq, xs, route, wq, ws)), out=y[:t])
+    ref, bound = F.linear_routed(xq, xs, route, wq, ws)
+    check_exact(y[:t], ref, bound)
+    assert bool((y[t] == 7).all())
 
 
 @pytest.mark.gpu
