@@ -473,7 +473,7 @@ struct Shape {
   double chunk, tile;
 };
 constexpr Shape kShapes[4] = {
-    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 5500}, {256, 64, 1, 1100, 7000}};
+    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 3700}, {256, 64, 1, 1100, 5000}};
 constexpr int kCus = 256;
 
 int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
@@ -511,7 +511,7 @@ Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
                     m * n > ((int64_t)1 << 26) / s))
         break;
       const double ns = shape_ns(kShapes[i], m, tiles * s, (chunks + s - 1) / s) +
-                        (s > 1 ? 2500.0 + 4.0 * (double)(m * n) * s / 4000.0 : 0.0);
+                        (s > 1 ? 4000.0 + 4.0 * (double)(m * n) * s / 4000.0 : 0.0);
       if (ns < best.ns) best = Plan{ns, i, s, 0};
     }
   }

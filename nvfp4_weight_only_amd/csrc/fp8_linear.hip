@@ -254,8 +254,8 @@ constexpr size_t kScalesLds = 65536;
 // Few rows of X: each CU streams its share of W through registers and reads all of X,
 // and the sum of both bounds it.  A CU takes 43 ns per KB from HBM (6.1 TB/s over
 // the chip; a CU by itself is no faster, so shares have to be even) and 31 ns per
-// KB of X from L2, the lines in flight being what is scarce; 4 us pass before and
-// after.  17408 x 5120 with M = 1, 16, 32, 48: 19.0, 21.2, 24.6 and 28.4 us.
+// KB of X from L2, the lines in flight being what is scarce; a launch takes 1 us and
+// a workgroup's start and sums 3.  17408 x 5120 with M = 1, 16, 32, 48: 19.0, 21.2, 24.6 and 28.4 us.
 struct Skinny {
   int mt = 1;        // 16 mt rows of X per workgroup
   int64_t span = 0;  // rows of W per workgroup; 0: scales too long for LDS
@@ -276,8 +276,8 @@ Skinny skinny_plan(int64_t m, int64_t n, int64_t k) {
   p.rounds = (n + cols * kMaxSpan - 1) / (cols * kMaxSpan);
   int64_t span = (n + cols * p.rounds - 1) / (cols * p.rounds);
   span = (span + 3) / 4 * 4;
-  const double wgs = (double)((n + span - 1) / span) * (double)gy;
-  p.ns = 4000.0 + (wgs > kCus ? wgs / kCus : 1.0) * (43.0 * (double)span + 31.0 * 16 * p.mt) * (double)k / 1024;
+  const double wgs = (double)((n + span - 1) / span) * (double)gy, turns = wgs > kCus ? wgs / kCus : 1.0;
+  p.ns = 1000.0 + turns * (3000.0 + (43.0 * (double)span + 31.0 * 16 * p.mt) * (double)k / 1024);
   if (fit >= 1) p.span = span;
   return p;
 }
@@ -290,7 +290,8 @@ bool skinny_supported(int64_t m, int64_t n, int64_t k) {
 }  // namespace
 
 // Measured, skinny against GEMM, us: M = 48 17408 x 5120 28.4 / 38.8, 5120 x 17408
-// 43.5 / 26.6; M = 96 5120 x 5120 21.8 / 18.1, 1024 x 2048 8.1 / 10.5.
+// 43.5 / 26.6; M = 96 5120 x 5120 21.8 / 18.1, 1024 x 2048 8.1 / 10.5; M = 200
+// 17408 x 128 13.3 / 6.4, 512 x 1024 5.4 / 6.5.
 // `split`: whether there is a workspace to split K with.
 static bool use_gemm(int64_t m, int64_t n, int64_t k, bool split) {
   if (!skinny_supported(m, n, k)) return true;

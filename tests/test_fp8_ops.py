@@ -378,11 +378,13 @@ def test_fp8_linear_large_exact(nv, m, n, k):
         assert not bool(bad.any()), f"workspace {ws}: {int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
 
 
-# Every tile of the GEMM with fewer chunks of K than its ring holds, as many, and more.
+# Every tile of the GEMM with fewer chunks of K than its ring holds, as many, and more, and with K split.
 @pytest.mark.gpu
 @pytest.mark.parametrize("m,n,k", [(1500, 9000, 128), (4100, 2050, 256), (2048, 9000, 272), (2048, 9000, 384),
                                    (260, 17408, 256), (200, 17408, 384), (260, 9000, 384), (2048, 700, 512),
-                                   (130, 17408, 2064), (4100, 260, 2064), (200, 9000, 2064)])
+                                   (130, 17408, 2064), (4100, 260, 2064), (200, 9000, 2064), (4100, 2050, 16),
+                                   (200, 17408, 16), (520, 129, 128), (520, 700, 256), (65, 17408, 2064),
+                                   (200, 17408, 4112), (100, 8192, 8192), (100, 6144, 8192)])
 def test_fp8_linear_few_chunks_exact(nv, m, n, k):
     d = [dev(a) for a in exact_operands(m, n, k, 750 + m + n + k)]
     x, w = decoded(d[0], d[1], 1), decoded(d[2], d[3], 128)
