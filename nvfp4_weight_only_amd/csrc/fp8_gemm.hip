@@ -47,8 +47,10 @@ struct GemmArgs {
   int64_t ld;       // values from one row of y to the next
   int kb, nb;
   int n_tiles, m_tiles;
-  // Split: slices of K, and their FP32 sums [slices, m, n] (slices = 1: none).
+  // Split: slices of K, and their FP32 sums [slices, m, np] (slices = 1: none), np
+  // being n rounded up to a multiple of 4.
   int slices;
+  int64_t np;
   float* part;
   // Grouped form: the sort's int32 arrays, pairs per token.
   const int32_t* groups;
@@ -406,12 +408,12 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   // Block t = i MT + j: lane (l16, g) holds row 16 j + l16 of X and rows 4 g +
   // 0..3 of the 16 of W, four neighbouring outputs of one row.
   const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN;
-  if (p.slices > 1) {  // FP32 sums of this slice; n is a multiple of 4 there
-    float* part = p.part + (int64_t)slice * p.m * p.n;
+  if (p.slices > 1) {  // FP32 sums of this slice
+    float* part = p.part + (int64_t)slice * p.m * p.np;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int r = 16 * (wm * MT + t % MT) + l16, col = 16 * (wn * NT + t / MT) + 4 * g;
-      if (r < rows && col < cols) *reinterpret_cast<f32x4_t*>(part + (m0 + r) * p.n + n0 + col) = acc[t];
+      if (r < rows && col < cols) *reinterpret_cast<f32x4_t*>(part + (m0 + r) * p.np + n0 + col) = acc[t];
     }
     return;
   }
@@ -447,17 +449,22 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
 
 // Sums of the slices in slice order, 4 outputs per thread: bound by its reads (4
 // slices of 333 x 5000: 5.6 us with the launch).
-__global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__ part, int slices, int64_t quads,
-                                                       uint16_t* __restrict__ y) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__ part, int slices, uint32_t quads,
+                                                       uint32_t n, uint16_t* __restrict__ y) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;
   f32x4_t s = reinterpret_cast<const f32x4_t*>(part)[i];
   for (int t = 1; t < slices; ++t) {
-    const f32x4_t o = reinterpret_cast<const f32x4_t*>(part)[(int64_t)t * quads + i];
+    const f32x4_t o = reinterpret_cast<const f32x4_t*>(part)[(size_t)t * quads + i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += o[e];
   }
-  reinterpret_cast<uint2*>(y)[i] = make_uint2(bf16x2_of(s[0], s[1]), bf16x2_of(s[2], s[3]));
+  if ((n & 3) == 0) {
+    reinterpret_cast<uint2*>(y)[i] = make_uint2(bf16x2_of(s[0], s[1]), bf16x2_of(s[2], s[3]));
+    return;
+  }
+  const uint32_t per_row = (n + 3) >> 2, row = i / per_row, col = 4 * (i - row * per_row);
+  for (uint32_t e = 0; e < 4 && col + e < n; ++e) y[(size_t)row * n + col + e] = (uint16_t)f32_to_bf16_rne(s[e]);
 }
 
 }  // namespace
@@ -507,7 +514,7 @@ Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
   for (int i = 0; i < 4; ++i) {
     const int64_t tiles = tiles_of(kShapes[i], m, n);
     for (int s = 1; s <= 8; ++s) {
-      if (s > 1 && (!split || (n & 3) != 0 || chunks < 4 * s || tiles * s > 2 * kCus ||
+      if (s > 1 && (!split || chunks < 4 * s || tiles * s > 2 * kCus ||
                     m * n > ((int64_t)1 << 26) / s))
         break;
       const double ns = shape_ns(kShapes[i], m, tiles * s, (chunks + s - 1) / s) +
@@ -553,7 +560,7 @@ double fp8_gemm_ns(int64_t m, int64_t n, int64_t k, bool split) { return gemm_pl
 
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = gemm_plan(m, n, k, true);
-  return p.slices > 1 ? 4 * m * n * p.slices : 0;
+  return p.slices > 1 ? 4 * m * ((n + 3) / 4 * 4) * p.slices : 0;
 }
 
 bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
@@ -570,7 +577,7 @@ void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, c
   const int64_t m_tiles = ((pairs + 127) / 128 + (experts < pairs ? experts : pairs) + 7) / 8;  // per XCD
   const int64_t n_tiles = (n + 255) / 256;
   const GemmArgs a{xq, xs, wq, ws, y, pairs, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128),
-                   (int)n_tiles, (int)m_tiles, 1, nullptr, groups, experts, topk};
+                   (int)n_tiles, (int)m_tiles, 1, 0, nullptr, groups, experts, topk};
   fp8_gemm_kernel<256, 128, 4, 2, 3, true><<<dim3((unsigned)(8 * n_tiles * m_tiles)), 512, 0, s>>>(a);
 }
 
@@ -578,7 +585,7 @@ void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, i
                      const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
   const Plan p = gemm_plan(m, n, k, workspace != nullptr);
   GemmArgs a{xq, xs, wq, ws, y, m, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128), 0, 0, p.slices,
-             static_cast<float*>(workspace), nullptr, 1, 1};
+             (n + 3) / 4 * 4, static_cast<float*>(workspace), nullptr, 1, 1};
   if (p.n1 == 0) {
     launch_shape(p.shape, a, s);
   } else {
@@ -589,8 +596,9 @@ void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, i
     launch_shape(2, a, s);
   }
   if (p.slices > 1) {
-    const int64_t quads = m * n / 4;
-    fp8_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a.part, p.slices, quads, y);
+    const int64_t quads = m * (a.np / 4);  // at most 2^24 and a few
+    fp8_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a.part, p.slices, (uint32_t)quads,
+                                                                          (uint32_t)n, y);
   }
 }
 

@@ -260,26 +260,28 @@ struct Skinny {
   int mt = 1;        // 16 mt rows of X per workgroup
   int64_t span = 0;  // rows of W per workgroup; 0: scales too long for LDS
   int64_t rounds = 1;
-  double ns = 0;
+  double ns = 0;  // estimated
 };
 
 // The rows of W in even shares, multiples of 4, of one workgroup per CU, or of as
-// many rounds of them as spans of at most 80 need.
+// many rounds of them as spans of at most 80 need; 64 rows of X at most per
+// workgroup, or fewer where W is small and X is what a CU reads (64 x 430 x 12032:
+// 30.0 us with 64, 12.8 with 16; 1024 x 2048, M = 64: 7.7 and 4.6).
 Skinny skinny_plan(int64_t m, int64_t n, int64_t k) {
-  Skinny p;
+  Skinny best;
+  best.ns = 1e300;
   const int64_t kb = (k + 127) / 128, fit = (int64_t)(kScalesLds / 64) / (kb | 1);
-  int64_t gy = (m + 63) / 64;
-  p.mt = (int)(((m + 15) / 16 + gy - 1) / gy);
-  if (p.mt > fit) p.mt = fit < 1 ? 1 : (int)fit;
-  gy = (m + 16 * p.mt - 1) / (16 * p.mt);
-  const int64_t cols = kCus / gy > 0 ? kCus / gy : 1;
-  p.rounds = (n + cols * kMaxSpan - 1) / (cols * kMaxSpan);
-  int64_t span = (n + cols * p.rounds - 1) / (cols * p.rounds);
-  span = (span + 3) / 4 * 4;
-  const double wgs = (double)((n + span - 1) / span) * (double)gy, turns = wgs > kCus ? wgs / kCus : 1.0;
-  p.ns = 1000.0 + turns * (3000.0 + (43.0 * (double)span + 31.0 * 16 * p.mt) * (double)k / 1024);
-  if (fit >= 1) p.span = span;
-  return p;
+  const int64_t most = (m + 15) / 16 < 4 ? (m + 15) / 16 : 4;
+  for (int64_t mt = most < fit ? most : fit; mt >= 1; --mt) {
+    const int64_t gy = (m + 16 * mt - 1) / (16 * mt), cols = kCus / gy > 0 ? kCus / gy : 1;
+    const int64_t rounds = (n + cols * kMaxSpan - 1) / (cols * kMaxSpan);
+    const int64_t span = ((n + cols * rounds - 1) / (cols * rounds) + 3) / 4 * 4;
+    const double wgs = (double)((n + span - 1) / span) * (double)gy, turns = wgs > kCus ? wgs / kCus : 1.0;
+    const double ns =
+        1000.0 + turns * (3000.0 + (43.0 * (double)span + 31.0 * 16 * (double)mt) * (double)k / 1024);
+    if (ns < best.ns) best = Skinny{(int)mt, span, rounds, ns};
+  }
+  return best;
 }
 
 // At least 4 rows of W per workgroup along x, at least 16 of X along y.

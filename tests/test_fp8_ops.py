@@ -384,7 +384,8 @@ def test_fp8_linear_large_exact(nv, m, n, k):
                                    (260, 17408, 256), (200, 17408, 384), (260, 9000, 384), (2048, 700, 512),
                                    (130, 17408, 2064), (4100, 260, 2064), (200, 9000, 2064), (4100, 2050, 16),
                                    (200, 17408, 16), (520, 129, 128), (520, 700, 256), (65, 17408, 2064),
-                                   (200, 17408, 4112), (100, 8192, 8192), (100, 6144, 8192)])
+                                   (200, 17408, 4112), (100, 8192, 8192), (100, 6144, 8192),
+                                   (31, 5003, 8208), (100, 6145, 8192), (64, 5122, 4096)])
 def test_fp8_linear_few_chunks_exact(nv, m, n, k):
     d = [dev(a) for a in exact_operands(m, n, k, 750 + m + n + k)]
     x, w = decoded(d[0], d[1], 1), decoded(d[2], d[3], 128)
