@@ -526,8 +526,7 @@ nvfp4_status nvfp4_silu_mul_fp8(const uint16_t* gate_up, int64_t rows, int64_t n
  * x [t_count, k], route [t_count, topk] int32 (device memory, 4-byte aligned),
  * y [t_count, topk, n] BF16.  An expert id outside [0, e) gives a row of zeros.
  * Rows of expert groups of any size, empty ones included.  With more than 512
- * pairs, or more than 4 per expert, k <= 2^23 and t_count * k < 2^32, else
- * NVFP4_ERR_UNSUPPORTED.  The workspace
+ * pairs, k <= 2^23 and t_count * k < 2^32, else NVFP4_ERR_UNSUPPORTED.  The workspace
  * (nvfp4_fp8_linear_grouped_workspace_bytes(t_count, topk, e) bytes, -1 for an
  * invalid shape) is required for t_count > 0 (NULL: NVFP4_ERR_NULL, fewer bytes:
  * NVFP4_ERR_SHAPE); any contents; not shared by calls in flight at the same time.

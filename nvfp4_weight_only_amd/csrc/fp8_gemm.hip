@@ -19,6 +19,8 @@
 // LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
 // piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
 // covers all banks.
+#include <math.h>
+
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -567,6 +569,19 @@ bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, 
   const int64_t pairs = t_count * topk, kb = (k + kChunk - 1) / kChunk;
   return k <= ((int64_t)1 << 23) && t_count <= ((int64_t)UINT32_MAX) / k && t_count <= (int64_t)UINT32_MAX / 4 / kb &&
          (pairs + 127) / 128 + experts + 8 <= ((int64_t)1 << 22) / ((n + 255) / 256);
+}
+
+// Experts that pairs with independent uniform ids are expected to choose.
+double fp8_experts_chosen(int64_t pairs, int64_t experts) {
+  return -(double)experts * expm1(-(double)pairs / (double)experts);
+}
+
+// Estimated time of sort and GEMM, for up to 128 pairs per expert.
+double fp8_gemm_grouped_ns(int64_t pairs, int64_t experts, int64_t n, int64_t k) {
+  const int64_t chunks = (k + kChunk - 1) / kChunk;
+  const double wgs = (double)((n + 255) / 256) * fp8_experts_chosen(pairs, experts);
+  const double rounds = ceil(wgs / kCus), filled = wgs < kCus ? wgs : kCus;
+  return 10500.0 + rounds * (3000.0 + (600.0 + 3.6 * filled) * (double)chunks);
 }
 
 void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,

@@ -308,19 +308,28 @@ int64_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   return use_gemm(m, n, k, true) ? fp8_gemm_workspace_bytes(m, n, k) : 0;
 }
 
-// Few pairs, and few per expert; of very few, more per expert, where the GEMM
-// has few tiles.  us, this against sort and GEMM: 128 experts 2048 x 4096 with 1,
-// 4, 8 pairs per expert 112 / 136, 201 / 198, 264 / 202; 16 of 4096 x 4096 with 4,
-// 6 50.9 / 49.3, 55.0 / 49.8; 8 of 14336 x 4096 with 8 96 / 120; 256 of 512 x 2048
-// with 2, 4 48.9 / 49.7, 68 / 56.
-static bool use_routed(int64_t pairs, int64_t experts, int64_t n) {
-  return pairs <= kMaxPairs && pairs <= (pairs <= 64 ? 8 : 4) * experts && n <= ((int64_t)1 << 26);
+// Few pairs without a sort, by estimate: 32 rows of W per workgroup, passed over
+// once per 16 pairs of the expert, and the workgroups that end at once; against
+// sort and GEMM, whose tiles of 256 rows of W slow each other down as they fill the
+// chip (fp8_gemm_grouped_ns).  us, this / those: 64 pairs, 8 of 184 x 448, 3.6 /
+// 12.3; 64, 8 of 4096 x 4096, 37 / 44; 128 of the same, 50 / 44; 512, 16 of 512 x
+// 2048, 23.6 / 20.4; 512, 128 of 2048 x 4096, 201 / 198.
+static bool use_routed(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
+  const int64_t pairs = t_count * topk;
+  if (pairs > kMaxPairs || n > ((int64_t)1 << 26) || k > ((int64_t)1 << 37)) return false;
+  if (!fp8_gemm_grouped_supported(t_count, topk, experts, n, k)) return true;
+  const double chosen = fp8_experts_chosen(pairs, experts), per = (double)pairs / chosen;
+  const double tiles = (double)((n + 31) / 32), passes = per <= 8.0 ? 1.0 : per / 16.0 + 0.5;
+  const double turns = chosen * tiles / kCus > 1.0 ? chosen * tiles / kCus : 1.0;
+  const double loads = (43.0 * 32 + 31.0 * (per < 16.0 ? per : 16.0)) * (double)k / 1024;
+  const double ns = 3500.0 + 700.0 * passes + turns * (500.0 + passes * loads) +
+                    100.0 * ((double)pairs - chosen) * tiles / kCus;
+  return ns < fp8_gemm_grouped_ns(pairs, experts, n, k);
 }
 
 bool fp8_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
   if (topk > ((int64_t)1 << 30) / t_count || experts > ((int64_t)1 << 28)) return false;
-  return use_routed(t_count * topk, experts, n) ? k <= ((int64_t)1 << 37)
-                                                : fp8_gemm_grouped_supported(t_count, topk, experts, n, k);
+  return use_routed(t_count, topk, experts, n, k) || fp8_gemm_grouped_supported(t_count, topk, experts, n, k);
 }
 
 // As few wavefronts as keep the number of passes over U blocks that MAXW allow.
@@ -367,7 +376,7 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
                                int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
                                void* workspace, hipStream_t s) {
   const int64_t pairs = t_count * topk;
-  if (use_routed(pairs, experts, n)) {
+  if (use_routed(t_count, topk, experts, n, k)) {
     const SkinnyArgs a{xq, xs, wq, ws, y, pairs, n, k, (int)((k + 127) / 128), (int)((n + 127) / 128), 32, route, experts,
                        topk};
     const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pairs);

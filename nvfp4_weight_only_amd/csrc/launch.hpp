@@ -160,6 +160,8 @@ void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, i
                      const float* ws, uint16_t* y, void* workspace, hipStream_t s);
 // The GEMM over the pairs sorted by expert (launch_group_sort).
 bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k);
+double fp8_experts_chosen(int64_t pairs, int64_t experts);
+double fp8_gemm_grouped_ns(int64_t pairs, int64_t experts, int64_t n, int64_t k);  // estimated time, with the sort's
 void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,
                              int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
                              hipStream_t s);
