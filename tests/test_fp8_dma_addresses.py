@@ -134,3 +134,32 @@ def test_fp8_gemm_tile_bound_leaves_a_workgroup_for_zero_rows():
 def test_fp8_gemm_largest_k_offsets_fit_32_bits():
     k = 1 << 23                     # fp8_gemm_supported
     assert 255 * k + 16 * 7 < 2 ** 32 and 4 * 255 * cdiv(k, CHUNK) < 2 ** 32
+
+
+@pytest.mark.parametrize("tiles", [1, 7, 8, 60, 61, 160, 544])
+def test_gemm_ids_reach_every_tile_once(tiles):
+    """The workgroups of a slice: XCD id % 8 takes consecutive tiles, whatever their number."""
+    more = tiles & 7
+    got = [(i & 7) * (tiles >> 3) + min(i & 7, more) + (i >> 3) for i in range(tiles)]
+    assert sorted(got) == list(range(tiles))
+
+
+@pytest.mark.parametrize("pairs,experts,seed", [(513, 3, 0), (1000, 8, 1), (4096, 128, 2), (600, 1000, 3), (520, 1, 4)])
+def test_grouped_places_reach_every_tile_and_zero_row_once(pairs, experts, seed):
+    """Every XCD's places: its eighth of the tiles in use, then zero rows, each of them from exactly one place."""
+    rng = np.random.default_rng(seed)
+    for invalid in (0, 1, pairs // 3, pairs):
+        counts = np.bincount(rng.integers(0, experts, pairs - invalid), minlength=experts)
+        used = int((-(-counts // 128)).sum())
+        per = cdiv(cdiv(pairs, 128) + min(experts, pairs), 8)    # m tiles per XCD
+        left, tiles, rows = 8 * per - used, [], []
+        for i in range(8 * per):
+            xcd, mt = i & 7, i >> 3
+            t0, t1 = used * xcd >> 3, used * (xcd + 1) >> 3
+            if mt < t1 - t0:
+                tiles.append(t0 + mt)
+            else:
+                assert left > 0
+                rows += list(range(pairs - invalid + xcd * per - t0 + mt - (t1 - t0), pairs, left))
+        assert sorted(tiles) == list(range(used))
+        assert sorted(rows) == list(range(pairs - invalid, pairs))

@@ -397,6 +397,26 @@ def test_fp8_linear_few_chunks_exact(nv, m, n, k):
     assert bool((y[m] == 7).all())
 
 
+# More rows, or columns, than one launch dimension holds of the kernels' smallest tiles.
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(1100000, 64, 128), (1048560, 16, 16), (1, 2 ** 26 + 77, 16), (20, 3000000, 16)])
+def test_fp8_linear_extreme_sizes_exact(nv, m, n, k):
+    torch.manual_seed(800 + m % 100)
+
+    def codes(*shape):
+        return torch.randint(0x30, 0x48, shape, device="cuda", dtype=torch.uint8)    # 0.5 .. 3.75, as exact_operands'
+    xq, wq = codes(m, k), codes(n, k)
+    xs = torch.full((m, 1), 2.0, device="cuda")
+    ws = 2.0 ** torch.randint(0, 2, (-(-n // 128), 1), device="cuda").float()
+    y = nv.fp8_linear(xq, xs, wq, ws)
+    x = xq.view(torch.float8_e4m3fn).float() * 2.0
+    for j in range(0, n, 1 << 20):
+        w = wq[j:j + (1 << 20)].view(torch.float8_e4m3fn).float()
+        w *= ws[j // 128:(j + len(w) + 127) // 128].repeat_interleave(128, 0)[:len(w)]
+        bad = y[:, j:j + len(w)] != (x @ w.T).bfloat16()
+        assert not bool(bad.any()), f"{int(bad.sum())} outputs differ, first {bad.nonzero()[:3].tolist()}"
+
+
 # Up to 64 rows: shares of 4, 20, 36, 52 (and 48, 56, 68 in more rounds) rows of W, which cross the blocks of 128 anywhere.
 @pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 17, 34, 64])
