@@ -25,12 +25,12 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace nvfp4 {
 namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) const void lds_t;
 
 constexpr int kChunk = 128;
 // Tiles with two stages only: how many chunks ahead of the loads to LDS lines are
@@ -58,46 +58,6 @@ struct GemmArgs {
   const int32_t* groups;
   int64_t experts, topk;
 };
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)(lds_t*)p; }
-
-// A pointer that is the same in every lane, in scalar registers.
-template <typename U>
-__device__ __forceinline__ const U* uniform(const U* p) {
-  const uint64_t b = (uint64_t)(uintptr_t)p;
-  return reinterpret_cast<const U*>(
-      ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
-      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b));
-}
-
-// A direct load to LDS from a uniform base: lane l's 16 bytes at offset off go
-// to lds + 16 l.  The asm block holds the wait states that the hardware leaves
-// to software on this path and that the compiler does not add around asm: five
-// between a vector instruction's write of a scalar register (the base may come
-// from a readfirstlane) and a memory instruction that reads it, one between a
-// write of M0 and a load to LDS.  No register result; the K loop waits for the
-// loads by count.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %2, %1" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)),
-               "s"(uniform(static_cast<const uint8_t*>(base))), "v"(off)
-               : "memory", "m0");
-}
-// The same for one load of 4 bytes per lane, to lds + 4 l.
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %2, %1" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)),
-               "s"(uniform(static_cast<const uint8_t*>(base))), "v"(off)
-               : "memory", "m0");
-}
-
-// 4 bytes of each lane's own address.
-__device__ __forceinline__ void dma4_lane(const void* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
-                   __builtin_amdgcn_readfirstlane(lds)),
-               "v"(p)
-               : "memory", "m0");
-}
 
 // At most N of this wavefront's loads still in flight, and its LDS reads done.
 template <int N>
@@ -200,8 +160,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     const int64_t rm = r < rows ? r : rows - 1;
     return GROUPED ? (int64_t)((uint32_t)perm[m0 + rm] / (uint32_t)p.topk) : rm;
   };
-  const uint8_t* wbase = uniform(wq + n0 * p.k);
-  const uint8_t* xbase = uniform(GROUPED ? p.xq : p.xq + m0 * p.k);
+  const uint8_t* wbase = uniform_ptr(wq + n0 * p.k);
+  const uint8_t* xbase = uniform_ptr(GROUPED ? p.xq : p.xq + m0 * p.k);
   uint32_t offw[LW], offx[LX];
 #pragma unroll
   for (int j = 0; j < LW; ++j) {
@@ -221,7 +181,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     sbase = ws + b0 * p.kb;
     soff = (uint32_t)(4 * b * p.kb);
   }
-  sbase = uniform(sbase);
+  sbase = uniform_ptr(sbase);
 
   // Lines brought into L2 ahead of their chunk's loads (one 4-byte read each, to
   // a part of LDS that nothing reads): the tiles that run on this XCD at the same
@@ -255,14 +215,14 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     Stage<TN, TM>& sg = stage[s];
     const int64_t k0 = (int64_t)cc * kChunk;
     const uint32_t bk = cc == p.kb - 1 ? back : 0u;
-    if (q < LW) dma16(wbase + k0, offw[q < LW ? q : 0] - bk, lds_addr(&sg.w[0]) + 1024 * w + 8192 * q);
+    if (q < LW) lds_dma16(wbase + k0, offw[q < LW ? q : 0] - bk, lds_addr(&sg.w[0]) + 1024 * w + 8192 * q);
     else if (q < LW + LX)
-      dma16(xbase + k0, offx[q >= LW && q < LW + LX ? q - LW : 0] - bk,
+      lds_dma16(xbase + k0, offx[q >= LW && q < LW + LX ? q - LW : 0] - bk,
             lds_addr(&sg.x[0]) + 1024 * w + 8192 * (q - LW));
     else if (q == LW + LX)
-      dma4(sbase + cc, soff, w < LX ? lds_addr(&sg.sx[64 * (w < LX ? w : 0)]) : lds_addr(&sg.sw[0]));
+      lds_dma4(sbase + cc, soff, w < LX ? lds_addr(&sg.sx[64 * (w < LX ? w : 0)]) : lds_addr(&sg.sw[0]));
     else
-      dma4_lane(pf + (int64_t)(cc + kAhead < last ? cc + kAhead : last) * kChunk, lds_addr(&sink[0]));
+      lds_dma4(pf + (int64_t)(cc + kAhead < last ? cc + kAhead : last) * kChunk, lds_addr(&sink[0]));
   };
   // This wavefront's loads of chunk c, in stage s, have landed.
   const auto finish = [&](int c, int s) {

@@ -30,6 +30,7 @@
 // right by 8h.
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -126,7 +127,6 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const uint32_t* __restr
 // ---------------------------------------------------------------------------
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) const void mx_lds_t;
 
 constexpr int kMxTile = 256;     // rows of W (n) and of X (m) per workgroup
 constexpr int kMxKC = 128;       // K elements per chunk (64 bytes per row, 4 scale bytes per row)
@@ -153,31 +153,6 @@ struct MxArgs {
   int64_t m, n, k;
   int n_tiles, m_tiles;
 };
-
-template <typename U>
-__device__ __forceinline__ uint32_t mx_lds_addr(const U* p) {
-  return (uint32_t)(uintptr_t)(mx_lds_t*)p;
-}
-
-__device__ __forceinline__ uint64_t mx_uniform_ptr(const void* base) {
-  const uint64_t b = (uint64_t)(uintptr_t)base;
-  return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
-         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
-}
-
-// One global_load_lds_dwordx4 (16 bytes per lane) / global_load_lds_dword (4
-// bytes per lane) from base + off (uniform 64-bit base, per-lane 32-bit offset)
-// to LDS lds + 16 * lane / lds + 4 * lane.  No register result; the kernel
-// waits for them with explicit vmcnt waits (they are its only global loads in
-// the K loop).
-__device__ __forceinline__ void mx_lds_dma16(const void* base, uint32_t off, uint32_t lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(mx_uniform_ptr(base)), "{m0}"(m0) : "memory");
-}
-__device__ __forceinline__ void mx_lds_dma4(const void* base, uint32_t off, uint32_t lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(mx_uniform_ptr(base)), "{m0}"(m0) : "memory");
-}
 
 template <int N>
 __device__ __forceinline__ void mx_wait_vmcnt() {
@@ -278,14 +253,14 @@ __global__ void __launch_bounds__(512) mx_gemm_kernel(MxArgs p) {
     const uint8_t* bw = p.wq + (int64_t)c * (kMxKC / 2);
     const uint8_t* bx = p.xq + (int64_t)c * (kMxKC / 2);
     MxStage& sg = stage[sidx];
-    const uint32_t lw = mx_lds_addr(&sg.w[0]), lx = mx_lds_addr(&sg.x[0]);
+    const uint32_t lw = lds_addr(&sg.w[0]), lx = lds_addr(&sg.x[0]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      mx_lds_dma16(bw, offw[j], lw + 1024 * (w + 8 * j));
-      mx_lds_dma16(bx, offx[j], lx + 1024 * (w + 8 * j));
+      lds_dma16(bw, offw[j], lw + 1024 * (w + 8 * j));
+      lds_dma16(bx, offx[j], lx + 1024 * (w + 8 * j));
     }
-    if (w < 4) mx_lds_dma4(p.ws + 4 * c, soff, mx_lds_addr(&sg.sw[64 * w4]));
-    else mx_lds_dma4(p.xs + 4 * c, soff, mx_lds_addr(&sg.sx[64 * w4]));
+    if (w < 4) lds_dma4(p.ws + 4 * c, soff, lds_addr(&sg.sw[64 * w4]));
+    else lds_dma4(p.xs + 4 * c, soff, lds_addr(&sg.sx[64 * w4]));
   };
 
   f32x16_t acc[NT][2];

@@ -28,13 +28,13 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace nvfp4 {
 
 namespace {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) const void pd_lds_t;
 
 constexpr int kPdBM = 128, kPdBN = 272, kPdBK = 64, kPdGroupK = 256;
 
@@ -107,34 +107,6 @@ struct PdLds {
   int32_t rowmap[kPdBM];  // grouped form: the output row (pair index) of each tile row
 };
 
-// One global_load_lds_dwordx4 from a per-lane 64-bit address (the weight group
-// loads mix the packed and the scale arrays in one instruction).
-__device__ __forceinline__ void pd_lds_dma16_ptr(const void* src, uint32_t lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(m0) : "memory");
-}
-
-// One global_load_lds_dwordx4: 16 bytes per lane from base + off (a
-// wavefront-uniform base and a per-lane 32-bit byte offset) to LDS address
-// lds + 16 * lane.  Written out rather than through the compiler builtin, whose
-// wait insertion loses track of which buffer a pending load writes at a loop
-// head and drains every load in flight; the instruction has no register
-// result, and the kernel orders LDS reads after it with explicit vmcnt waits.
-// M0 is declared clobbered, so the compiler keeps nothing of its own there.
-__device__ __forceinline__ void pd_lds_dma16(const void* base, uint32_t off, uint32_t lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
-  const uint64_t b = (uint64_t)(uintptr_t)base;
-  // readfirstlane returns int: widen through uint32_t, never by sign extension.
-  const uint64_t bs = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
-                      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(bs), "{m0}"(m0) : "memory");
-}
-
-template <typename U>
-__device__ __forceinline__ uint32_t pd_lds_addr(const U* p) {
-  return (uint32_t)(uintptr_t)(pd_lds_t*)p;
-}
-
 template <int N>
 __device__ __forceinline__ void pd_wait_vmcnt() {
   static_assert(N >= 0 && N <= 63, "vmcnt range");
@@ -186,7 +158,7 @@ __device__ __forceinline__ PdDma pd_dma_begin(const PdArgs& p, int64_t m0, int64
   const int gb = (t >> 2) & 1;
   (void)n0;
   return PdDma{reinterpret_cast<const uint8_t*>(p.x + m0 * p.k) + (int64_t)tc * (2 * kPdBK), gc,
-               pd_lds_addr(&L.xs[xst]), pd_lds_addr(&L.wg[gb])};
+               lds_addr(&L.xs[xst]), lds_addr(&L.wg[gb])};
 }
 
 // Load instruction I of a step (place in group P): 0..3 activations, then at a
@@ -194,13 +166,13 @@ __device__ __forceinline__ PdDma pd_dma_begin(const PdArgs& p, int64_t m0, int64
 template <int P, int I>
 __device__ __forceinline__ void pd_dma_one(const PdSrc& src, const PdDma& d, int w) {
   if constexpr (I < kPdLX) {
-    pd_lds_dma16(d.xb, src.x[I], d.xs + 1024 * (w + 4 * I));
+    lds_dma16(d.xb, src.x[I], d.xs + 1024 * (w + 4 * I));
   } else if constexpr (P == 0 && I < kPdLX + kPdLW) {
     constexpr int i = I - kPdLX;
     const int q0 = 64 * (w + 4 * i);
     const int q = q0 < kPdWLast ? q0 : kPdWLast;
     const int64_t step = (src.wscale >> i) & 1u ? kPdGroupK / 16 : kPdGroupK / 2;
-    pd_lds_dma16_ptr(src.w[i] + d.gc * step, d.wg + 16 * q);
+    lds_dma16(src.w[i] + d.gc * step, d.wg + 16 * q);
   }
 }
 

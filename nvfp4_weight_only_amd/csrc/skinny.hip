@@ -32,6 +32,7 @@
 // K terms; only the FP32 summation order changes).
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace nvfp4 {
 
@@ -326,34 +327,6 @@ __global__ void __launch_bounds__(64 * T) skinny_kernel(SkinnyArgs p) {
 // reads of chunk c + 1's operands and runs chunk c's MFMAs on the operands
 // read in step c - 1, so the LDS reads overlap the decode.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) const void sk_lds_t;
-
-// One global_load_lds_dwordx4: 16 bytes from each lane's `src` to LDS byte
-// address lds + 16 * lane (lds wave-uniform, in M0).  Written out rather than
-// through the compiler builtin: for the builtin, the compiler's wait insertion
-// loses track of which stage a pending load writes at the loop head and waits
-// for every load in flight (vmcnt(0)) once per ring turn, which drains the
-// pipeline.  The instruction has no register result, so nothing the compiler
-// allocates can be overwritten by the load in flight; the kernel's explicit
-// vmcnt waits order the LDS reads after it.  M0 is declared clobbered, so the
-// compiler keeps nothing of its own there across the statement.
-__device__ __forceinline__ void sk_lds_dma16(const void* src, uint32_t lds) {
-  const uint32_t base = __builtin_amdgcn_readfirstlane(lds);  // uniform per wavefront by construction
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(base) : "memory");
-}
-
-// The same with the nontemporal hint, for the weight rows: each instruction
-// reads whole lines of data that no other workgroup reads.
-__device__ __forceinline__ void sk_lds_dma16_nt(const void* src, uint32_t lds) {
-  const uint32_t base = __builtin_amdgcn_readfirstlane(lds);  // uniform per wavefront by construction
-  asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(base) : "memory");
-}
-
-template <typename U>
-__device__ __forceinline__ uint32_t sk_lds_addr(const U* p) {
-  return (uint32_t)(uintptr_t)(const sk_lds_t*)p;
-}
-
 template <int N>
 __device__ __forceinline__ void sk_wait_vmcnt() {
   static_assert(N >= 0 && N <= 63, "vmcnt range");
@@ -471,16 +444,16 @@ __device__ __forceinline__ void sk_dma_issue(const SkinnyArgs& p, const SkDmaSrc
                                              int c0, SkStage<MX, TT>& S, uint4* sg, int lane) {
   const int cc = ci < nc ? ci : nc - 1;
 #pragma unroll
-  for (int i = 0; i < LW; ++i) sk_lds_dma16_nt(src.w[i] + (int64_t)cc * 128, sk_lds_addr(&S.w[src.wslot[i]]));
+  for (int i = 0; i < LW; ++i) lds_dma16_nt(src.w[i] + (int64_t)cc * 128, lds_addr(&S.w[src.wslot[i]]));
 #pragma unroll
-  for (int i = 0; i < LX; ++i) sk_lds_dma16(src.x[i] + (int64_t)cc * kSkChunk, sk_lds_addr(&S.x[src.xslot[i]]));
+  for (int i = 0; i < LX; ++i) lds_dma16(src.x[i] + (int64_t)cc * kSkChunk, lds_addr(&S.x[src.xslot[i]]));
   if ((ci & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
       // this lane's chunk of the group; chunks past the weight's end read the last chunk's scales
       const bool in = (int64_t)(c0 + ci + (lane & 3)) < p.chunks;
       const uint8_t* a = in ? src.s[i] + (int64_t)ci * 16 : p.scales + src.sclamp[i];
-      sk_lds_dma16(a, sk_lds_addr(&sg[src.sslot[i]]));
+      lds_dma16(a, lds_addr(&sg[src.sslot[i]]));
     }
   }
 }

@@ -43,6 +43,7 @@
 // result is the same bits on every run.
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace nvfp4 {
 
@@ -300,18 +301,6 @@ __global__ void __launch_bounds__(64 * kSmWaves) small_m_kernel(SmArgs p) {
 // products run.  Weights load into registers as above.  Only the wavefront
 // reads its own area, so the K loop has no barrier; the wait for a quad's copy
 // is a vmcnt that also covers its weight loads (loads complete in order).
-typedef __attribute__((address_space(3))) const void sm_lds_t;
-
-template <typename U>
-__device__ __forceinline__ uint32_t sm_lds_addr(const U* ptr) {
-  return (uint32_t)(uintptr_t)(const sm_lds_t*)ptr;
-}
-
-// 64 lanes x 16 bytes from per-lane global addresses to LDS bytes [lds, lds + 1024).
-__device__ __forceinline__ void sm_lds_dma16(const void* src, uint32_t lds) {
-  const uint32_t base = __builtin_amdgcn_readfirstlane(lds);  // uniform per wavefront by construction
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(base) : "memory");
-}
 
 template <int N>
 __device__ __forceinline__ void sm_wait_vmcnt() {
@@ -369,7 +358,7 @@ __global__ void __launch_bounds__(64 * kSmWaves) small_m_xl_kernel(SmArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) xoff[i][mt] = (uint32_t)(rr * 256 + (((4 * i + g) ^ (rr & 15)) * 16));
   }
-  const uint32_t area = sm_lds_addr(&lds[0]) + (uint32_t)(w * 2 * XB);
+  const uint32_t area = lds_addr(&lds[0]) + (uint32_t)(w * 2 * XB);
   const char* lds_bytes = reinterpret_cast<const char*>(&lds[0]) + w * 2 * XB;
 
   f32x4_t acc[T][NMT];
@@ -388,7 +377,7 @@ __global__ void __launch_bounds__(64 * kSmWaves) small_m_xl_kernel(SmArgs p) {
     auto copy_x = [&](int j, int buf) {
       const int64_t q = qw + kSmWaves * j;
 #pragma unroll
-      for (int d = 0; d < D; ++d) sm_lds_dma16(xsrc[d] + q * kSmQuadK, area + (uint32_t)(buf * XB + d * 1024));
+      for (int d = 0; d < D; ++d) lds_dma16(xsrc[d] + q * kSmQuadK, area + (uint32_t)(buf * XB + d * 1024));
     };
     // Quad j: weights in wq, activations in area buf.  In issue order, quad
     // j's weight loads and copy precede quad j + 1's 2 T weight loads, so
