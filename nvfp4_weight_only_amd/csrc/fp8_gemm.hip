@@ -24,13 +24,12 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "fp8_mfma.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
 
 namespace nvfp4 {
 namespace {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kChunk = 128;
 // Tiles with two stages only: how many chunks ahead of the loads to LDS lines are
@@ -64,14 +63,6 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N >= 0 && N <= 63, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
-}
-
-__device__ __forceinline__ i32x8_t frag(const uint4& a, const uint4& b) {
-  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-
-__device__ __forceinline__ f32x4_t mfma128(const i32x8_t& a, const i32x8_t& b) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
@@ -245,8 +236,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   const uint32_t rw = lane_off + 128 * 16 * wn * NT;
   const char* const lds0 = reinterpret_cast<const char*>(&stage[0]);
   const auto read = [&](uint32_t off, int rows16) {
-    return frag(*reinterpret_cast<const uint4*>(lds0 + off + 2048 * rows16),
-                *reinterpret_cast<const uint4*>(lds0 + (off ^ 16) + 2048 * rows16));
+    return mfma_frag(*reinterpret_cast<const uint4*>(lds0 + off + 2048 * rows16),
+                     *reinterpret_cast<const uint4*>(lds0 + (off ^ 16) + 2048 * rows16));
   };
   const auto meet = [&]() {
     asm volatile("" ::: "memory");
@@ -282,6 +273,9 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   }
   a[0] = read(rw, 0);
   sw = stage[0].sw[((int)(n0 & 127) + 16 * wn * NT) >> 7];
+  // No scalar load is under way in the loop, where each wait for one would be a wait
+  // for all reads of LDS (2048 x 17408 x 5120: 194.5 us without, 192.5 with).
+  __builtin_amdgcn_s_waitcnt(0xC07F);
   // Sums of the last blocks: block t is scaled behind the matrix instruction of
   // block t + 2, so that the multiply-adds never wait for it.
   f32x4_t d[4];
@@ -291,6 +285,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
 #pragma unroll
   for (int j = 0; j < MT; ++j) f[j] = 0.0f;
   int sidx = 0;
+  uint64_t far = 0;  // lanes that met two scales for which is_far
   // REST, NEXT: the rest of chunk c - 1 + ST, and the first loads of chunk c + ST, are there to be issued.
   const auto step = [&](int c, auto rest, auto next) {
     constexpr bool REST = decltype(rest)::value, NEXT = decltype(next)::value;
@@ -300,6 +295,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     f_old[0] = f[MT - 2], f_old[1] = f[MT - 1];
 #pragma unroll
     for (int j = 0; j < MT; ++j) f[j] = sx[j] * sw;
+    const float fw = sw;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       if (i < NT - 1) {
@@ -319,6 +315,15 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
         const int t = i * MT + j, u = (t + T - 2) % T;
         d[t & 3] = mfma128(a[i & 1], b[j]);
         __builtin_amdgcn_sched_barrier(0);
+        if (i == 1 && j == 0) {  // here nothing waits for it
+          bool normal = true;
+#pragma unroll
+          for (int q = 0; q < MT; ++q) normal &= is_normal(f[q]);
+          if (__builtin_amdgcn_ballot_w64(!normal) != 0) {
+#pragma unroll
+            for (int q = 0; q < MT; ++q) far |= __builtin_amdgcn_ballot_w64(is_far(sx[q], fw));
+          }
+        }
         if (i == NT - 1) {
           b[j] = read(sn + rx, j);
           sx[j] = stage[sidx].sx[16 * wm * MT + l16 + 16 * j];
@@ -368,26 +373,63 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   __syncthreads();
 
   // Block t = i MT + j: lane (l16, g) holds row 16 j + l16 of X and rows 4 g +
-  // 0..3 of the 16 of W, four neighbouring outputs of one row.
+  // 0..3 of the 16 of W, four neighbouring outputs of one row.  The FP32 sums of a
+  // slice go to the workspace.  A BF16 tile goes through LDS (the stages are free),
+  // so that the stores to Y are whole rows: [TM rows][TN columns], 16-byte pieces
+  // swizzled as above.
   const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN;
-  if (p.slices > 1) {  // FP32 sums of this slice
-    float* part = p.part + (int64_t)slice * p.m * p.np;
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int r = 16 * (wm * MT + t % MT) + l16, col = 16 * (wn * NT + t / MT) + 4 * g;
-      if (r < rows && col < cols) *reinterpret_cast<f32x4_t*>(part + (m0 + r) * p.np + n0 + col) = acc[t];
-    }
-    return;
-  }
-  // The BF16 tile goes through LDS (the stages are free), so that the stores to
-  // Y are whole rows: [TM rows][TN columns], 16-byte pieces swizzled as above.
   uint16_t* yt = reinterpret_cast<uint16_t*>(&stage[0]);
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const int r = 16 * (wm * MT + t % MT) + l16, col = 16 * (wn * NT + t / MT) + 4 * g;
+  const auto put_sums = [&](int i, int j, const f32x4_t& v) {
+    const int r = 16 * (wm * MT + j) + l16, col = 16 * (wn * NT + i) + 4 * g;
+    float* part = p.part + (int64_t)slice * p.m * p.np;
+    if (r < rows && col < cols) *reinterpret_cast<f32x4_t*>(part + (m0 + r) * p.np + n0 + col) = v;
+  };
+  const auto put_tile = [&](int i, int j, const f32x4_t& v) {
+    const int r = 16 * (wm * MT + j) + l16, col = 16 * (wn * NT + i) + 4 * g;
     *reinterpret_cast<uint2*>(yt + r * TN + 8 * ((col >> 3) ^ (r & 7)) + (col & 4)) =
-        make_uint2(bf16x2_of(acc[t][0], acc[t][1]), bf16x2_of(acc[t][2], acc[t][3]));
+        make_uint2(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]));
+  };
+  if (far == 0) {
+    if (p.slices > 1) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) put_sums(t / MT, t % MT, acc[t]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < T; ++t) put_tile(t / MT, t % MT, acc[t]);
+    }
+  } else {
+    // Two scales, neither 0, whose product is no normal FP32 number: this wavefront's
+    // sums again, block by block from memory, with the scales taken apart.  (So in the
+    // loop above, for every tile: 2048 x 17408 x 5120 198.5 us, 192.5 this way.)
+    const uint8_t* xq = GROUPED ? p.xq : p.xq + m0 * p.k;
+    const float* xs = GROUPED ? p.xs : p.xs + m0 * p.kb;
+#pragma unroll 1
+    for (int t = 0; t < T; ++t) {
+      const int64_t wr = n0 + 16 * (wn * NT + t / MT) + l16, wc = wr < p.n ? wr : p.n - 1;
+      const int64_t xr = x_row(16 * (wm * MT + t % MT) + l16);
+      const uint8_t *wp = wq + wc * p.k + 16 * g, *xp = xq + xr * p.k + 16 * g;
+      const float *wsp = ws + (wc >> 7) * p.kb, *xsp = xs + xr * p.kb;
+      f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        // Pieces past the end of a row: the row's last piece of W, zeros of X.
+        const int64_t k0 = (int64_t)kChunk * c, end = p.k - 16 - 16 * g;
+        const bool in0 = k0 <= end, in1 = k0 + 64 <= end;
+        const int64_t o0 = in0 ? k0 : end, o1 = in1 ? k0 + 64 : end;
+        const auto load = [](const uint8_t* q) { return *reinterpret_cast<const uint4*>(q); };
+        const uint4 z = make_uint4(0, 0, 0, 0), x0 = load(xp + o0), x1 = load(xp + o1);
+        const float sw = wsp[c], sx = xsp[c];
+        const int ew = scale_exp(sw), ex = scale_exp(sx);
+        const f32x4_t d = mfma128(mfma_frag(load(wp + o0), load(wp + o1)), mfma_frag(in0 ? x0 : z, in1 ? x1 : z), ew, ex);
+        const float f = scale_rest(sx, ex) * scale_rest(sw, ew);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(d[e], f, v[e]);
+      }
+      if (p.slices > 1) put_sums(t / MT, t % MT, v);
+      else put_tile(t / MT, t % MT, v);
+    }
   }
+  if (p.slices > 1) return;
   __syncthreads();
   typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
   const bool vec = (p.n & 7) == 0 && (p.ld & 7) == 0;

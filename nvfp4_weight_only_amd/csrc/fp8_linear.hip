@@ -2,25 +2,18 @@
 //   y[i, j] = BF16( sum_b xs[i, b] ws[j / 128, b] sum_{k in b} x[i, k] w[j, k] ).
 //
 // The inner sum over a block of 128 is one 16x16x128 matrix instruction per
-// 16 x 16 outputs (C = 0); its result is scaled and added in FP32 by the vector
-// ALU.  The weights are the A operand (rows n) and the activations the B
+// 16 x 16 outputs (C = 0); its result is scaled (fp8_mfma.hpp) and added in FP32 by
+// the vector ALU.  The weights are the A operand (rows n) and the activations the B
 // operand (columns m), so the four results of a lane belong to one activation
-// row: one factor xs[m, b] ws[n / 128, b] per lane.  Both operands place the
+// row: one factor per lane.  Both operands place the
 // same element of K at the same position, whatever the order within the block.
 
 #include "device_common.hpp"
+#include "fp8_mfma.hpp"
 #include "launch.hpp"
 
 namespace nvfp4 {
 namespace {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4_t mfma128(const uint4& a0, const uint4& a1, const uint4& b0, const uint4& b1) {
-  const i32x8_t a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-  const i32x8_t b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-}
 
 struct SkinnyArgs {
   const uint8_t* xq;  // [rows of x, k]
@@ -82,6 +75,30 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
   }
   const int ld = p.kb | 1;  // an odd number of words from row to row
   const auto sx = [&](int t, int b) -> float { return SXL ? sxl[(16 * t + r) * ld + b] : xsp[t][b]; };
+  // The scales of block b: ea and fa by this lane's row of W as an operand (r) and as
+  // an output (4 g), eb and fb of the row of X; of zeros for a block that is not `in`.
+  struct Factors {
+    int ea[NT], eb[MT];
+    float fa[NT], fb[MT];
+  };
+  const auto factors = [&](int b, bool in) {
+    Factors v;
+    const float sw = wsp[b], sw2 = wsp2[b];
+    const int e = scale_exp(sw), e2 = scale_exp(sw2);
+    const float f = scale_rest(sw, e), f2 = scale_rest(sw2, e2);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      v.ea[t] = 16 * t + r < rest ? e : e2;
+      v.fa[t] = in ? (16 * t + 4 * g < rest ? f : f2) : 0.0f;
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const float s = in ? sx(t, b) : 0.0f;
+      v.eb[t] = scale_exp(s);
+      v.fb[t] = scale_rest(s, v.eb[t]);
+    }
+    return v;
+  };
   const auto load = [](const uint8_t* q) { return *reinterpret_cast<const uint4*>(q); };
   f32x4_t acc[T];
 #pragma unroll
@@ -107,15 +124,14 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
   const auto step = [&](int b, const Blocks& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int bb = b + u < b1 ? b + u : b1 - 1;
-      const float sw = wsp[bb], sw2 = wsp2[bb];
-      float f[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) f[t] = sx(t, bb);
+      const bool in = u == 0 || b + u < b1;
+      const Factors s = factors(in ? b + u : b1 - 1, in);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const float ft = b + u < b1 ? f[t % MT] * (16 * (t / MT) + 4 * g < rest ? sw : sw2) : 0.0f;
-        const f32x4_t d = mfma128(v.w[u][t / MT][0], v.w[u][t / MT][1], v.x[u][t % MT][0], v.x[u][t % MT][1]);
+        const int i = t / MT, j = t % MT;
+        const float ft = s.fb[j] * s.fa[i];
+        const f32x4_t d = mfma128(mfma_frag(v.w[u][i][0], v.w[u][i][1]), mfma_frag(v.x[u][j][0], v.x[u][j][1]), s.ea[i],
+                                  s.eb[j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], ft, acc[t][e]);
       }
@@ -153,12 +169,15 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& p, const uint8_t* 
     const int64_t k0 = 128 * (int64_t)full, end = p.k - 16 - 16 * g;
     const bool in0 = k0 <= end, in1 = k0 + 64 <= end;
     const int64_t o0 = in0 ? k0 : end, o1 = in1 ? k0 + 64 : end;
+    const Factors s = factors(full, true);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      const uint8_t* xt = xp[t % MT];
+      const int i = t / MT, j = t % MT;
+      const uint8_t *wt = wp[i], *xt = xp[j];
       const uint4 z = make_uint4(0, 0, 0, 0), x0 = load(xt + o0), x1 = load(xt + o1);
-      const f32x4_t d = mfma128(load(wp[t / MT] + o0), load(wp[t / MT] + o1), in0 ? x0 : z, in1 ? x1 : z);
-      const float f = sx(t % MT, full) * (16 * (t / MT) + 4 * g < rest ? wsp : wsp2)[full];
+      const f32x4_t d = mfma128(mfma_frag(load(wt + o0), load(wt + o1)), mfma_frag(in0 ? x0 : z, in1 ? x1 : z), s.ea[i],
+                                s.eb[j]);
+      const float f = s.fb[j] * s.fa[i];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(d[e], f, acc[t][e]);
     }
@@ -347,7 +366,7 @@ static void launch_skinny_shape(const SkinnyArgs& a, hipStream_t s) {
 // (MT = 4, NT = 5).
 template <int MT>
 static void launch_skinny(const SkinnyArgs& a, int64_t rounds, hipStream_t s) {
-  if (a.span <= 16) return launch_skinny_shape<MT, 1, 4 - MT / 2, 8>(a, s);
+  if (a.span <= 16) return launch_skinny_shape<MT, 1, MT == 1 ? 4 : MT == 2 ? 3 : 2, 8>(a, s);
   if (a.span <= 32) return launch_skinny_shape<MT, 2, MT <= 2 ? 2 : 1, 8>(a, s);
   if (a.span <= 48) return launch_skinny_shape<MT, 3, 1, 8>(a, s);
   if constexpr (MT < 4)

@@ -487,6 +487,50 @@ def test_fp8_linear_infinite_scales(nv, m, k):
     assert torch.equal(nv.fp8_linear_grouped(*args[:2], route, args[2][None], args[3][None]).cpu()[:, 0], want)
 
 
+def far_scales(kind, m, n, k, seed, e=None):
+    """Operands whose results are normal BF16 numbers although products of two scales are not FP32 numbers, or are
+    subnormal ones.  "above": codes of 1 .. 7 steps of 2^-9 (a block's sum is below 2^-5) and products of scales up to
+    2.25 2^130; "below": codes 128 .. 448 (a block's sum, all of one sign, is above 2^18) and products of scales from
+    2.25 2^-143.  The exponents are split unevenly between the two scales, another way in each block of K.  Every third
+    block of K of X is zero, and all from the twelfth on; there the product of the scales is as large as it can be."""
+    rng = np.random.default_rng(seed)
+    lead, kb, nb = () if e is None else (e,), -(-k // 128), -(-n // 128)
+    lo, hi, top = (0x01, 0x08, 130) if kind == "above" else (0x70, 0x7F, -140)
+    xq = rng.integers(lo, hi, size=(m, k)).astype(np.uint8)
+    wq = rng.integers(lo, hi, size=lead + (n, k)).astype(np.uint8)
+    split = rng.integers(5, 120, size=kb) if kind == "above" else rng.integers(-120, -5, size=kb)
+    xs = np.exp2(split[None] - rng.integers(0, 2, size=(m, kb))) * rng.choice([1.0, 1.5], size=(m, kb))
+    ws = np.exp2(top - split - rng.integers(0, 2, size=lead + (nb, kb))) * rng.choice([1.0, 1.5], size=lead + (nb, kb))
+    for b in (b for b in range(kb) if b % 3 == 2 or b >= 12):
+        xq[:, 128 * b:128 * (b + 1)] = 0
+        xs[:, b], ws[..., b] = 1.5 * 2.0 ** 127, 1.5 * 2.0 ** 127
+    return xq, xs.astype(np.float32), wq, ws.astype(np.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["above", "below"])
+@pytest.mark.parametrize("m,n,k", [(1, 16, 128), (3, 300, 1040), (20, 1000, 400), (40, 9003, 272), (64, 5000, 400),
+                                   (3, 20, 131200), (100, 513, 384), (200, 5122, 784), (300, 1030, 2064),
+                                   (700, 9000, 400), (2048, 2100, 272)])
+def test_fp8_linear_far_scales(nv, m, n, k, kind):
+    """The scales are applied without forming a product that leaves FP32's range."""
+    xq, xs, wq, ws = far_scales(kind, m, n, k, 1200 + m + n + k)
+    ref, bound = F.linear(xq, xs, wq, ws)
+    assert 2.0 ** -126 < np.abs(ref).min() and np.abs(ref).max() < 2.0 ** 127
+    y = nv.fp8_linear(*map(dev, (xq, xs, wq, ws)))
+    check(y, ref, bound, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["above", "below"])
+@pytest.mark.parametrize("t,topk,e,n,k", [(4, 2, 5, 130, 400), (300, 4, 6, 300, 1040)])
+def test_fp8_linear_grouped_far_scales(nv, t, topk, e, n, k, kind):
+    xq, xs, wq, ws = far_scales(kind, t, n, k, 1300 + t, e)
+    route = routing("uniform", t, topk, e, 1301 + t)
+    ref, bound = F.linear_routed(xq, xs, route, wq, ws)
+    check(nv.fp8_linear_grouped(*map(dev, (xq, xs, route, wq, ws))), ref, bound, k)
+
+
 def routing(kind, t, topk, e, seed):
     rng = np.random.default_rng(seed)
     if kind == "uniform":
