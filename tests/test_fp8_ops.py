@@ -245,6 +245,38 @@ def test_rmsnorm_fp8_odd_rows(nv):
         assert np.all(codes[row] == 0x7F) and np.isnan(scales[row]).all()
 
 
+# Standard deviations of h and of the weight whose products overflow FP32, are subnormal, or are 0 there.
+@pytest.mark.gpu
+@pytest.mark.parametrize("h_exp,g_exp", [(50, 90), (-70, -70), (-100, -90), (-100, -20), (-40, -88)])
+@pytest.mark.parametrize("m,k", [(3, 400), (600, 1040), (2, 40016)])
+def test_rmsnorm_fp8_far_products(nv, m, k, h_exp, g_exp):
+    """The codes are those of the exact products, whatever range they are in."""
+    eps = 2.0 ** -126
+    h = WL.bf16_bits_from_f32(WL.f32_from_bf16_bits(WL.normal_bf16((m, k), 1.0, 310 + k)) * np.float32(2.0 ** h_exp))
+    g = WL.bf16_bits_from_f32(WL.f32_from_bf16_bits(WL.normal_bf16((k,), 1.0, 311 + k)) * np.float32(2.0 ** g_exp))
+    h[-1, 128:256] = 0                       # a block of zeros, and one with an ordinary product
+    g[:4] = WL.bf16_bits_from_f32(np.float32([2.0 ** (60 if g_exp < 0 else -60)] * 4))
+    codes, scales, _ = nv.rmsnorm_fp8(bf16(h), bf16(g), eps)
+    rc, rs = F.norm(f64(h), f64(g), eps)
+    assert np.array_equal(host(codes), rc)
+    # rs, and its rounding where it is subnormal: the largest value's (then divided by 448) and its own.
+    assert np.all(np.abs(host(scales) - rs) <= norm_tolerance(k) * rs + 1.01 * 2.0 ** -150)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [1024, 40960])
+def test_rmsnorm_fp8_value_not_finite(nv, k):
+    """A value that overflows though its product does not: scale NaN and codes 0x7F in its block alone."""
+    x, g = np.zeros((2, k), dtype=np.float32), np.ones(k, dtype=np.float32)
+    x[:, 200], g[200], x[1, 600] = 1.0, 3e38, 1.0
+    codes, scales, _ = nv.rmsnorm_fp8(*(bf16(WL.bf16_bits_from_f32(a)) for a in (x, g)), EPS)
+    codes, scales = host(codes), host(scales)
+    nan = np.zeros(scales.shape, dtype=bool)
+    nan[:, 1] = True
+    assert np.array_equal(np.isnan(scales), nan) and np.all(codes[:, 128:256] == 0x7F)
+    assert codes[1, 600] == 0x7E and not np.delete(codes, [*range(128, 256), 600], axis=1).any()
+
+
 def silu_check(codes, scales, v):
     """Codes and scales of v (float64) when v is computed in FP32 within delta: log2(e) g is carried in two floats and
     the hardware's exp2 is within 1 ulp, so exp has about 4 u; the sum, division and product add u each, and the
