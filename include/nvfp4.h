@@ -488,7 +488,8 @@ nvfp4_status nvfp4_linear_w4a4(const uint16_t* x, int64_t m, int64_t n, int64_t 
  * nvfp4_silu_mul_fp8: gate_up [rows, 2 n] BF16 (the merged projection's output,
  * gate columns first) -> v = silu(gate) * up, silu(g) = g / (1 + exp(-g)), as
  * codes [rows, n] and scales [rows, ceil(n / 128)] (1 x 128); n a multiple of
- * 16.
+ * 16.  v is computed in FP32, without a step that leaves its range before v does;
+ * silu of a gate below -174 (less than 2^-243) counts as 0.
  */
 nvfp4_status nvfp4_fp8_quantize(const uint16_t* w, int64_t count, int64_t rows, int64_t k, int64_t block_rows,
                                 uint8_t* codes, float* scales, void* stream);

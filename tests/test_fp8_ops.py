@@ -321,6 +321,32 @@ def test_silu_mul_fp8_extremes(nv):
             assert np.isfinite(host(scales)[1]).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [400, 5120, 40000])
+def test_silu_mul_fp8_far_gates(nv, n):
+    """silu(gate) far below FP32's normal range, or a subnormal gate's half, times an up that brings it back: blocks
+    whose gates have one size each, the ups another, so that every block's results are normal FP32 numbers."""
+    gates = np.float32([-86, -87.5, -88, -95, -104, -120, -150, -170, 2.0 ** -130, -2.0 ** -128, 2.0 ** -120, -64, -30, -3])
+    ups = np.float32([1, 1, 2, 64, 1e8, 1e20, 1e37, 3e38, 1e30, 1e20, 1e10, 1e-5, 1e38, 1e38])
+    rng = np.random.default_rng(410 + n)
+    b = np.empty((gates.size, 2 * n), dtype=np.float32)
+    b[:, :n] = gates[:, None] * rng.uniform(0.97, 1, (1, n))
+    b[:, n:] = ups[:, None] * rng.uniform(0.01, 1, (1, n)) * rng.choice([-1, 1], (1, n))
+    bits = WL.bf16_bits_from_f32(b)
+    codes, scales = nv.silu_mul_fp8(bf16(bits))
+    v = F.silu_mul(f64(bits[:, :n]), f64(bits[:, n:]))
+    amax = F.block_amax(v, 1)
+    assert 2.0 ** -122 < amax.min() and np.abs(v).max() < 2.0 ** 127
+    # As silu_check, with the FP32 rounding of a subnormal value (2^-150) on top.
+    delta, scales = 16 * U, host(scales)
+    assert np.all(np.abs(scales - amax / 448) <= delta * amax / 448 + 2.0 ** -149)
+    q, got = np.abs(F.quotients(v, 1)), F.values(host(codes))
+    step = np.exp2(np.floor(np.log2(np.maximum(q, 2.0 ** -6))) - 3)
+    low = 448 * 2.0 ** -150 / F.spread(amax, 1, *v.shape)
+    assert np.all(np.abs(np.abs(got) - q) <= step / 2 + delta * q + low)
+    assert np.all((got == 0) | (np.sign(got) == np.sign(v)))
+
+
 def operands(m, n, k, seed, e=None):
     """Random operands with uneven scales, as host arrays."""
     rng = np.random.default_rng(seed)
