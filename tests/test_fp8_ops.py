@@ -167,6 +167,20 @@ def test_fp8_quantize_bit_exact(nv, shape, block_rows):
     assert same_scales(scales, rs) and np.array_equal(host(codes), rc)
 
 
+# More than 32768 blocks of 1 x 128, so several per thread: 32 .. 63 blocks a row (two, with one scalar division per
+# workgroup), 64 and more and fewer than 16 (four, with and without), 16 .. 31 (one).
+MANY_BLOCKS = [(2048, 5120), (1100, 4112), (900, 8208), (4200, 1040), (33000, 16), (2100, 2064)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k", MANY_BLOCKS)
+def test_fp8_quantize_many_blocks(nv, m, k):
+    bits = WL.normal_bf16((m, k), 0.02, 110 + k)
+    codes, scales = nv.fp8_quantize(bf16(bits))
+    rc, rs = F.quantize(f64(bits), 1)
+    assert same_scales(scales, rs) and np.array_equal(host(codes), rc)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_fp8_quantize_crafted(nv, block_rows):
@@ -221,6 +235,44 @@ def test_rmsnorm_fp8(nv, m, k, mode):
     rc, rs = F.norm(h, f64(gb), EPS)
     assert np.array_equal(host(codes), rc)
     assert np.all(np.abs(host(scales) - rs) <= norm_tolerance(k) * rs)
+
+
+# More than 512 rows: three pieces a thread, in workgroups of one wavefront and of several.
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k", [(600, 16), (700, 400), (513, 5120), (515, 1552)])
+@pytest.mark.parametrize("mode", ["plain", "residual", "in place"])
+def test_rmsnorm_fp8_many_rows(nv, m, k, mode):
+    test_rmsnorm_fp8(nv, m, k, mode)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,k", [(6, 384), (600, 384), (530, 5120), (6, 40960)])
+@pytest.mark.parametrize("mode", ["plain", "residual", "in place"])
+def test_rmsnorm_fp8_odd_rows_everywhere(nv, m, k, mode):
+    """The odd rows below in every kernel: rows of zeros, a block of zeros, a square that overflows, infinities (one of
+    them made by the residual's addition) and NaN change their own rows only."""
+    xb, rb, gb = WL.normal_bf16((m, k), 1.0, 320 + k), WL.normal_bf16((m, k), 1.0, 321 + k), WL.normal_bf16((k,), 1.0, 322 + k)
+    xb[0], rb[0], xb[m - 1, 128:256], rb[m - 1, 128:256] = 0, 0, 0, 0
+    xb[1, k - 1] = WL.bf16_bits_from_f32(np.float32([3e38]))[0]
+    xb[2, 7], xb[3, 300] = 0x7F80, 0x7FC0
+    xb[4, 9], rb[4, 9] = 0x7F00, 0x7F00 if mode != "plain" else 0       # 2^127 twice: infinite when added
+    x, r, g = bf16(xb), bf16(rb), bf16(gb)
+    h = f64(xb)
+    if mode == "plain":
+        codes, scales, _ = nv.rmsnorm_fp8(x, g, EPS)
+    else:
+        want = (x.float() + r.float()).bfloat16()
+        h = host(want)
+        codes, scales, out = nv.rmsnorm_fp8(x, g, EPS, residual=r, residual_out=r if mode == "in place" else None)
+        assert torch.equal(out.nan_to_num(1e30, 2e30), want.nan_to_num(1e30, 2e30))
+    codes, scales = host(codes), host(scales)
+    assert not codes[0].any() and not scales[0].any()
+    assert not codes[m - 1, 128:256].any() and scales[m - 1, 1] == 0
+    for row in (1, 2, 3, 4):
+        assert np.all(codes[row] == 0x7F) and np.isnan(scales[row]).all(), row
+    rc, rs = F.norm(h[5:], f64(gb), EPS)
+    assert np.array_equal(codes[5:], rc)
+    assert np.all(np.abs(scales[5:] - rs) <= norm_tolerance(k) * rs)
 
 
 @pytest.mark.gpu
@@ -297,6 +349,12 @@ def test_silu_mul_fp8(nv, m, n):
     b = WL.normal_bf16((m, 2 * n), 3.0, 400 + n)
     codes, scales = nv.silu_mul_fp8(bf16(b))
     silu_check(host(codes), host(scales), F.silu_mul(f64(b[:, :n]), f64(b[:, n:])))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", MANY_BLOCKS)
+def test_silu_mul_fp8_many_blocks(nv, m, n):
+    test_silu_mul_fp8(nv, m, n)
 
 
 @pytest.mark.gpu
