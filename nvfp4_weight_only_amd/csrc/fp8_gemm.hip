@@ -19,24 +19,18 @@
 // LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
 // piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
 // covers all banks.
-#include <math.h>
-
 #include <type_traits>
 
 #include "device_common.hpp"
 #include "fp8_mfma.hpp"
+#include "fp8_tiles.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kChunk = 128;
-// Tiles with two stages only: how many chunks ahead of the loads to LDS lines are
-// brought into L2 (256 x 256 over 2048 x 16384 x 5120: 174 us without, 170 with;
-// with three stages the lines come early enough, and the lines in flight are what
-// is scarce: 64 x 5120 x 17408 30 us without, 38 with).
-constexpr int kAhead = 2;
+using namespace fp8_tiles;
 
 struct GemmArgs {
   const uint8_t* xq;
@@ -93,10 +87,6 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = w % WN, wm = w / WN;
 
-  // Workgroups go to the 8 XCDs round-robin by id.  An XCD's share of a slice, its
-  // ids in order, are consecutive tiles, m tiles first: a tile's rows of W are
-  // fetched into that XCD's L2 once (333 x 5000 x 17392, 60 tiles a slice: 74.6
-  // us with the tiles in the order of the ids, 69.8 so).
   int id = (int)blockIdx.x, slice = 0, nt, mt;
   if constexpr (GROUPED) {
     nt = (id >> 3) % p.n_tiles, mt = (id >> 3) / p.n_tiles;
@@ -104,8 +94,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     const int tiles = p.n_tiles * p.m_tiles;
     slice = id / tiles;
     id -= slice * tiles;
-    const int xcd = id & 7, more = tiles & 7;
-    id = xcd * (tiles >> 3) + (xcd < more ? xcd : more) + (id >> 3);
+    id = tile_of_id(id, tiles);
     nt = id / p.m_tiles, mt = id % p.m_tiles;
   }
   const int64_t n0 = (int64_t)nt * TN;
@@ -121,10 +110,10 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     // the rows of X too are fetched into its L2 once (2048 x 4096, 256 tokens, top 8
     // of 128: 213 us so, 277 by n tile).  The workgroups left over
     // write zero rows for the pairs whose id is out of range.
-    const int64_t used = tile_off[p.experts], xcd = id & 7, t0 = used * xcd >> 3, tn = (used * (xcd + 1) >> 3) - t0;
+    const int64_t used = tile_off[p.experts], xcd = id & 7, t0 = first_of_xcd(used, xcd), tn = first_of_xcd(used, xcd + 1) - t0;
     if (mt >= tn) {
-      const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN, left = 8 * (int64_t)p.m_tiles - used;
-      for (int64_t i = pair_off[p.experts] + xcd * p.m_tiles - t0 + mt - tn; i < p.m; i += left)
+      const int64_t cols = p.n - n0 < TN ? p.n - n0 : TN, left = left_places(used, p.m_tiles);
+      for (int64_t i = pair_off[p.experts] + left_rank(xcd, p.m_tiles, t0, tn, mt); i < p.m; i += left)
         for (int64_t c = tid; c < cols; c += 512) p.y[perm[i] * p.ld + n0 + c] = 0;
       return;
     }
@@ -143,12 +132,9 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     ws += lo * p.nb * p.kb;
   }
 
-  // This wavefront's loads: instruction j fills rows 8 (w + 8 j) .. + 7, lane l
-  // row + l / 8, physical piece l % 8.  Rows past N or the tile's rows of X
-  // repeat the last one (their results are not stored).
-  const int lrow = lane >> 3, piece = (lane & 7) ^ lrow;  // row & 7 == lrow
-  const auto x_row = [&](int r) -> int64_t {              // the row of X behind row r of the tile
-    const int64_t rm = r < rows ? r : rows - 1;
+  const int piece = lane_piece(lane);
+  const auto x_row = [&](int r) -> int64_t {  // the row of X behind row r of the tile
+    const int64_t rm = row_or_last(r, rows);
     return GROUPED ? (int64_t)((uint32_t)perm[m0 + rm] / (uint32_t)p.topk) : rm;
   };
   const uint8_t* wbase = uniform_ptr(wq + n0 * p.k);
@@ -156,64 +142,54 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   uint32_t offw[LW], offx[LX];
 #pragma unroll
   for (int j = 0; j < LW; ++j) {
-    const int64_t r = 8 * (w + 8 * j) + lrow, rn = n0 + r < p.n ? r : p.n - 1 - n0;
-    offw[j] = (uint32_t)(rn * p.k + 16 * piece);
+    offw[j] = piece_offset(row_or_last(load_row(w, j, lane), p.n - n0), p.k, piece);
   }
 #pragma unroll
-  for (int j = 0; j < LX; ++j) offx[j] = (uint32_t)(x_row(8 * (w + 8 * j) + lrow) * p.k + 16 * piece);
+  for (int j = 0; j < LX; ++j) offx[j] = piece_offset(x_row(load_row(w, j, lane)), p.k, piece);
   // Scales: wavefront w < LX the rows 64 w .. + 63 of X, the others the blocks of W.
   const float* sbase;
   uint32_t soff;
   if (w < LX) {
     sbase = GROUPED ? p.xs : p.xs + m0 * p.kb;
-    soff = (uint32_t)(4 * x_row(64 * w + lane) * p.kb);
+    soff = scale_offset(x_row(64 * w + lane), p.kb);
   } else {
-    const int64_t b0 = n0 / 128, b = b0 + lane < p.nb ? lane : p.nb - 1 - b0;
+    const int64_t b0 = n0 / 128;
     sbase = ws + b0 * p.kb;
-    soff = (uint32_t)(4 * b * p.kb);
+    soff = scale_offset(row_or_last(lane, p.nb - b0), p.kb);
   }
   sbase = uniform_ptr(sbase);
 
   // Lines brought into L2 ahead of their chunk's loads (one 4-byte read each, to
-  // a part of LDS that nothing reads): the tiles that run on this XCD at the same
-  // time and share rows of W (m tiles, up to 8) or of X share this work.
+  // a part of LDS that nothing reads).
   static_assert(!L2 || (!GROUPED && TN + TM <= 512), "one line per lane");
   const uint8_t* pf = nullptr;
   if constexpr (L2) {
-    const int share_w = p.m_tiles < 8 ? p.m_tiles : 8, share_x = 32 / share_w < p.n_tiles ? 32 / share_w : p.n_tiles;
-    const int lines_w = (TN + share_w - 1) / share_w, lines_x = (TM + share_x - 1) / share_x;
-    const int i = 8 * lane + w;
-    if (i < lines_w || i >= lines_w + lines_x) {
-      const int r = (i < lines_w ? i : 0) * share_w + mt % share_w;
-      pf = wbase + (n0 + r < p.n ? r : p.n - 1 - n0) * p.k;
-    } else {
-      const int r = (i - lines_w) * share_x + nt % share_x;
-      pf = xbase + x_row(r < TM ? r : TM - 1) * p.k;
-    }
+    const Line l = line_ahead(TN, TM, p.n_tiles, p.m_tiles, nt, mt, w, lane);
+    pf = l.of_w ? wbase + row_or_last(l.row, p.n - n0) * p.k : xbase + x_row(l.row) * p.k;
   }
   // Chunks of this slice.
-  const int c0 = (int)((int64_t)p.kb * slice / p.slices), c1 = (int)((int64_t)p.kb * (slice + 1) / p.slices);
+  const int c0 = first_chunk(p.kb, slice, p.slices), c1 = first_chunk(p.kb, slice + 1, p.slices);
   const int last = c1 - 1;
   // A last, short chunk: pieces past the end of K are read from the row's last
   // one, and X's are set to zero in LDS when they have landed (finish).  W's keep
   // the copy: times zero, or NaN where that row's sum is NaN by its own piece.
-  const int ktail = (int)(p.k & (kChunk - 1));
-  const bool past = ktail != 0 && 16 * piece >= ktail;
-  const uint32_t back = past ? (uint32_t)(16 * piece - (ktail - 16)) : 0u;
+  const int ktail = tail_of(p.k);
+  const bool past = past_end(ktail, piece);
+  const uint32_t back = step_back(ktail, piece);
 
   // Load q (of NL) of chunk cc into stage s.
   const auto issue = [&](int q, int cc, int s) {
     Stage<TN, TM>& sg = stage[s];
     const int64_t k0 = (int64_t)cc * kChunk;
     const uint32_t bk = cc == p.kb - 1 ? back : 0u;
-    if (q < LW) lds_dma16(wbase + k0, offw[q < LW ? q : 0] - bk, lds_addr(&sg.w[0]) + 1024 * w + 8192 * q);
+    if (q < LW) lds_dma16(wbase + k0, offw[q < LW ? q : 0] - bk, lds_addr(&sg.w[0]) + load_dst(w, q));
     else if (q < LW + LX)
       lds_dma16(xbase + k0, offx[q >= LW && q < LW + LX ? q - LW : 0] - bk,
-            lds_addr(&sg.x[0]) + 1024 * w + 8192 * (q - LW));
+            lds_addr(&sg.x[0]) + load_dst(w, q - LW));
     else if (q == LW + LX)
       lds_dma4(sbase + cc, soff, w < LX ? lds_addr(&sg.sx[64 * (w < LX ? w : 0)]) : lds_addr(&sg.sw[0]));
     else
-      lds_dma4(pf + (int64_t)(cc + kAhead < last ? cc + kAhead : last) * kChunk, lds_addr(&sink[0]));
+      lds_dma4(pf + (int64_t)chunk_ahead(cc, last) * kChunk, lds_addr(&sink[0]));
   };
   // This wavefront's loads of chunk c, in stage s, have landed.
   const auto finish = [&](int c, int s) {
@@ -229,9 +205,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
 #pragma unroll
   for (int t = 0; t < T; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // Byte offsets in a stage of this lane's first row of each operand, at the
-  // lane group's first piece (2 g); the second piece is the offset ^ 16.
-  const uint32_t lane_off = (uint32_t)(128 * l16 + 16 * ((2 * g) ^ (l16 & 7)));
+  // Byte offsets in a stage of this lane's first row of each operand.
+  const uint32_t lane_off = read_offset(l16, g);
   const uint32_t rx = lane_off + (uint32_t)(sizeof(uint4) * TN * 8) + 128 * 16 * wm * MT;
   const uint32_t rw = lane_off + 128 * 16 * wn * NT;
   const char* const lds0 = reinterpret_cast<const char*>(&stage[0]);
@@ -405,17 +380,16 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
     const float* xs = GROUPED ? p.xs : p.xs + m0 * p.kb;
 #pragma unroll 1
     for (int t = 0; t < T; ++t) {
-      const int64_t wr = n0 + 16 * (wn * NT + t / MT) + l16, wc = wr < p.n ? wr : p.n - 1;
+      const int64_t wr = row_or_last(n0 + 16 * (wn * NT + t / MT) + l16, p.n);
       const int64_t xr = x_row(16 * (wm * MT + t % MT) + l16);
-      const uint8_t *wp = wq + wc * p.k + 16 * g, *xp = xq + xr * p.k + 16 * g;
-      const float *wsp = ws + (wc >> 7) * p.kb, *xsp = xs + xr * p.kb;
+      const uint8_t *wp = wq + wr * p.k, *xp = xq + xr * p.k;
+      const float *wsp = ws + (wr >> 7) * p.kb, *xsp = xs + xr * p.kb;
       f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
       for (int c = c0; c < c1; ++c) {
         // Pieces past the end of a row: the row's last piece of W, zeros of X.
-        const int64_t k0 = (int64_t)kChunk * c, end = p.k - 16 - 16 * g;
-        const bool in0 = k0 <= end, in1 = k0 + 64 <= end;
-        const int64_t o0 = in0 ? k0 : end, o1 = in1 ? k0 + 64 : end;
+        bool in0, in1;
+        const int64_t o0 = again_offset(c, p.k, g, 0, &in0), o1 = again_offset(c, p.k, g, 1, &in1);
         const auto load = [](const uint8_t* q) { return *reinterpret_cast<const uint4*>(q); };
         const uint4 z = make_uint4(0, 0, 0, 0), x0 = load(xp + o0), x1 = load(xp + o1);
         const float sw = wsp[c], sx = xsp[c];
@@ -475,102 +449,37 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__
 
 namespace {
 
-// Tile shapes: ns per chunk of 128 and per tile (first loads and epilogue), as
-// measured with a CU's slots filled.  256 x 256 reaches 1.9 PFLOP/s over the chip,
-// the smaller ones less (more LDS reads and loads per product), but they have finer
-// steps for sizes that leave CUs idle.
-struct Shape {
-  int tn, tm, per_cu;
-  double chunk, tile;
-};
-constexpr Shape kShapes[4] = {
-    {256, 256, 1, 1900, 9000}, {256, 128, 1, 1000, 7000}, {128, 64, 2, 1050, 3700}, {256, 64, 1, 1100, 5000}};
-constexpr int kCus = 256;
-
-int64_t tiles_of(const Shape& s, int64_t m, int64_t n) { return ((n + s.tn - 1) / s.tn) * ((m + s.tm - 1) / s.tm); }
-
-// Estimated ns of the tiles over the chip, each K slice `chunks` long.  A chunk
-// takes its compute time or that of its loads: 21 ns per KB that L2 holds, 43 per
-// KB from HBM, where W comes from for one of the m tiles.
-double shape_ns(const Shape& s, int64_t m, int64_t wgs, int64_t chunks) {
-  const double m_tiles = (double)((m + s.tm - 1) / s.tm), slots = (double)kCus * s.per_cu;
-  const double loads = 0.125 * (s.tn * (21.0 + 22.0 / m_tiles) + 21.0 * s.tm);
-  // Half-filled CUs: a workgroup alone on its CU computes in a little under half the pair's time.
-  const bool alone = s.per_cu == 2 && wgs <= kCus;
-  const double compute = alone ? 400.0 : s.chunk, load = s.per_cu == 2 && !alone ? 2.0 * loads : loads;
-  const double rounds = (double)((wgs + (int64_t)slots - 1) / (int64_t)slots);
-  return rounds * (s.tile + (compute > load ? compute : load) * (double)chunks);
-}
-
-struct Plan {
-  double ns = 1e300;
-  int shape = 0, slices = 1;
-  int64_t n1 = 0;  // columns of the 256 x 256 tiles that come first (0: one launch)
-};
-
-// The cheapest of: one shape; one shape with K split (the slices' sums take a
-// write, a read and a second launch); whole rounds of 256 x 256 tiles and a
-// second launch with small tiles for the columns left over, which would
-// otherwise occupy a round by themselves.
-Plan gemm_plan(int64_t m, int64_t n, int64_t k, bool split) {
-  const int64_t chunks = (k + kChunk - 1) / kChunk;
-  Plan best;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t tiles = tiles_of(kShapes[i], m, n);
-    for (int s = 1; s <= 8; ++s) {
-      if (s > 1 && (!split || chunks < 4 * s || tiles * s > 2 * kCus ||
-                    m * n > ((int64_t)1 << 26) / s))
-        break;
-      const double ns = shape_ns(kShapes[i], m, tiles * s, (chunks + s - 1) / s) +
-                        (s > 1 ? 4000.0 + 4.0 * (double)(m * n) * s / 4000.0 : 0.0);
-      if (ns < best.ns) best = Plan{ns, i, s, 0};
-    }
-  }
-  const int64_t m_tiles = (m + 255) / 256, n_tiles = (n + 255) / 256;
-  const int64_t rounds = n_tiles * m_tiles / kCus, cols = rounds * kCus / m_tiles;  // n tiles of whole rounds
-  if (rounds > 0 && cols > 0 && cols < n_tiles) {
-    const double ns = shape_ns(kShapes[0], m, cols * m_tiles, chunks) + 3000.0 +
-                      shape_ns(kShapes[2], m, tiles_of(kShapes[2], m, n - 256 * cols), chunks);
-    if (ns < best.ns) best = Plan{ns, 0, 1, 256 * cols};
-  }
-  return best;
-}
-
-template <int TN, int TM, int WN, int WM, int ST>
+template <int S>
 void launch_tiles(GemmArgs a, hipStream_t s) {
-  a.n_tiles = (int)((a.n + TN - 1) / TN);
-  a.m_tiles = (int)((a.m + TM - 1) / TM);
-  fp8_gemm_kernel<TN, TM, WN, WM, ST, false>
+  constexpr Shape t = kShapes[S];
+  a.n_tiles = (int)((a.n + t.tn - 1) / t.tn);
+  a.m_tiles = (int)((a.m + t.tm - 1) / t.tm);
+  fp8_gemm_kernel<t.tn, t.tm, t.wn, t.wm, t.stages, false>
       <<<dim3((unsigned)((int64_t)a.n_tiles * a.m_tiles * a.slices)), 512, 0, s>>>(a);
 }
 
 void launch_shape(int shape, const GemmArgs& a, hipStream_t s) {
   switch (shape) {
-    case 0: launch_tiles<256, 256, 2, 4, 2>(a, s); break;
-    case 1: launch_tiles<256, 128, 4, 2, 3>(a, s); break;
-    case 2: launch_tiles<128, 64, 4, 2, 3>(a, s); break;
-    default: launch_tiles<256, 64, 8, 1, 3>(a, s); break;
+    case 0: launch_tiles<0>(a, s); break;
+    case 1: launch_tiles<1>(a, s); break;
+    case 2: launch_tiles<2>(a, s); break;
+    default: launch_tiles<3>(a, s); break;
   }
 }
 
 }  // namespace
 
-// 32-bit offsets inside a tile, and at most 2^32 threads.
-bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) {
-  return k <= ((int64_t)1 << 23) && (m + 63) / 64 <= ((int64_t)1 << 22) / ((n + 127) / 128);
-}
+bool fp8_gemm_supported(int64_t m, int64_t n, int64_t k) { return gemm_supported(m, n, k); }
 
 double fp8_gemm_ns(int64_t m, int64_t n, int64_t k, bool split) { return gemm_plan(m, n, k, split).ns; }
 
 int64_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   const Plan p = gemm_plan(m, n, k, true);
-  return p.slices > 1 ? 4 * m * ((n + 3) / 4 * 4) * p.slices : 0;
+  return p.slices > 1 ? 4 * m * sums_per_row(n) * p.slices : 0;
 }
 
 bool fp8_gemm_grouped_supported(int64_t t_count, int64_t topk, int64_t experts, int64_t n, int64_t k) {
-  const int64_t pairs = t_count * topk, kb = (k + kChunk - 1) / kChunk;
-  return k <= ((int64_t)1 << 23) && t_count <= ((int64_t)UINT32_MAX) / k && t_count <= (int64_t)UINT32_MAX / 4 / kb &&
-         (pairs + 127) / 128 + experts + 8 <= ((int64_t)1 << 22) / ((n + 255) / 256);
+  return grouped_supported(t_count, topk, experts, n, k);
 }
 
 // Experts that pairs with independent uniform ids are expected to choose.
@@ -589,28 +498,25 @@ double fp8_gemm_grouped_ns(int64_t pairs, int64_t experts, int64_t n, int64_t k)
 void launch_fp8_gemm_grouped(const uint8_t* xq, const float* xs, int64_t topk, const int32_t* groups, int64_t pairs,
                              int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
                              hipStream_t s) {
-  // Fewer than one tile past pairs / 128 for each expert that has pairs; at least
-  // one workgroup is left for rows of zeros if there are any.
-  const int64_t m_tiles = ((pairs + 127) / 128 + (experts < pairs ? experts : pairs) + 7) / 8;  // per XCD
+  const int64_t m_tiles = grouped_m_tiles(pairs, experts);  // per XCD
   const int64_t n_tiles = (n + 255) / 256;
   const GemmArgs a{xq, xs, wq, ws, y, pairs, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128),
                    (int)n_tiles, (int)m_tiles, 1, 0, nullptr, groups, experts, topk};
-  fp8_gemm_kernel<256, 128, 4, 2, 3, true><<<dim3((unsigned)(8 * n_tiles * m_tiles)), 512, 0, s>>>(a);
+  constexpr Shape t = kShapes[kGroupedShape];
+  fp8_gemm_kernel<t.tn, t.tm, t.wn, t.wm, t.stages, true><<<dim3((unsigned)(8 * n_tiles * m_tiles)), 512, 0, s>>>(a);
 }
 
 void launch_fp8_gemm(const uint8_t* xq, const float* xs, int64_t m, int64_t n, int64_t k, const uint8_t* wq,
                      const float* ws, uint16_t* y, void* workspace, hipStream_t s) {
   const Plan p = gemm_plan(m, n, k, workspace != nullptr);
   GemmArgs a{xq, xs, wq, ws, y, m, n, k, n, (int)((k + kChunk - 1) / kChunk), (int)((n + 127) / 128), 0, 0, p.slices,
-             (n + 3) / 4 * 4, static_cast<float*>(workspace), nullptr, 1, 1};
-  if (p.n1 == 0) {
-    launch_shape(p.shape, a, s);
-  } else {
-    a.n = p.n1, a.nb = (int)(p.n1 / 128);
-    launch_shape(0, a, s);
-    a.wq = wq + p.n1 * k, a.ws = ws + p.n1 / 128 * a.kb, a.y = y + p.n1;
-    a.n = n - p.n1, a.nb = (int)((n - p.n1 + 127) / 128);
-    launch_shape(2, a, s);
+             sums_per_row(n), static_cast<float*>(workspace), nullptr, 1, 1};
+  Launch l[2];
+  const int launches = launches_of(p, n, l);
+  for (int i = 0; i < launches; ++i) {  // n0: a multiple of 256
+    a.wq = wq + l[i].n0 * k, a.ws = ws + l[i].n0 / 128 * a.kb, a.y = y + l[i].n0;
+    a.n = l[i].n, a.nb = (int)((l[i].n + 127) / 128);
+    launch_shape(l[i].shape, a, s);
   }
   if (p.slices > 1) {
     const int64_t quads = m * (a.np / 4);  // at most 2^24 and a few
