@@ -405,6 +405,54 @@ def test_silu_mul_fp8_far_gates(nv, n):
     assert np.all((got == 0) | (np.sign(got) == np.sign(v)))
 
 
+# More blocks and rows than one dimension of a launch holds, and offsets that pass 32 bits: the same as call by call on
+# parts (every block stands for itself).
+@pytest.mark.gpu
+def test_fp8_quantize_more_blocks_than_a_launch(nv):
+    part = bf16(WL.normal_bf16((4096, 16), 1.0, 420))
+    codes, scales = nv.fp8_quantize(part)
+    reps, rest = 2 ** 16, 37                                   # 2^28 rows of one block, and a few
+    x = torch.cat([part.repeat(reps, 1), part[:rest]])
+    got, got_scales = nv.fp8_quantize(x)
+    del x
+    assert bool((got[:4096 * reps].view(reps, 4096, 16) == codes).all()) and torch.equal(got[4096 * reps:], codes[:rest])
+    assert bool((got_scales[:4096 * reps].view(reps, 4096, 1) == scales).all())
+    assert torch.equal(got_scales[4096 * reps:], scales[:rest])
+
+
+@pytest.mark.gpu
+def test_fp8_producers_rows_of_2_to_the_28(nv):
+    """Rows whose offsets do not fit the 32 bits of the form for shorter ones."""
+    rows, k, part = 2, 2 ** 28 + 2 ** 16, 2 ** 16
+    torch.manual_seed(421)
+    x = torch.randn((rows, k), device="cuda", dtype=torch.bfloat16)
+    for block_rows in (1, 128):
+        codes, scales = nv.fp8_quantize(x, block_rows)
+        for j in range(0, k, 64 * part):
+            piece = x[:, j:j + 64 * part].contiguous()
+            want, want_scales = nv.fp8_quantize(piece, block_rows)
+            assert torch.equal(codes[:, j:j + 64 * part], want)
+            assert torch.equal(scales[:, j // 128:(j + 64 * part) // 128], want_scales)
+    up = torch.randn((rows, k), device="cuda", dtype=torch.bfloat16)
+    codes, scales = nv.silu_mul_fp8(torch.cat([x, up], 1))
+    want, want_scales = nv.silu_mul_fp8(torch.cat([x.view(-1, part), up.view(-1, part)], 1))
+    assert torch.equal(codes.view(-1, part), want) and torch.equal(scales.view(-1, part // 128), want_scales)
+
+
+@pytest.mark.gpu
+def test_fp8_producers_more_rows_than_a_launch_dimension(nv):
+    m, k = 2 ** 20 + 37, 16
+    xb, gb = WL.normal_bf16((m, k), 1.0, 422), WL.normal_bf16((k,), 1.0, 423)
+    x, g = bf16(xb), bf16(gb)
+    codes, scales, h = nv.rmsnorm_fp8(x, g, EPS, residual=x)
+    for part in (slice(0, m // 2), slice(m // 2, m)):
+        for got, want in zip((codes, scales, h), nv.rmsnorm_fp8(x[part], g, EPS, residual=x[part])):
+            assert torch.equal(got[part], want)
+    codes, scales = nv.fp8_quantize(x.view(m, 1, k), 128)      # one block of 128 x 128 per matrix
+    want, want_scales = nv.fp8_quantize(x, 1)
+    assert torch.equal(codes.view(m, k), want) and torch.equal(scales.view(m, 1), want_scales)
+
+
 def operands(m, n, k, seed, e=None):
     """Random operands with uneven scales, as host arrays."""
     rng = np.random.default_rng(seed)
