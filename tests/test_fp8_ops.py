@@ -685,6 +685,30 @@ def test_fp8_linear_far_scales(nv, m, n, k, kind):
     check(y, ref, bound, k)
 
 
+# Every tile shape, two launches, slices of K; the last three in which one row in seven has such scales, and the others
+# ordinary ones and zeros (of codes and scale) where the far rows have zeros and the largest scales.
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["above", "below"])
+@pytest.mark.parametrize("m,n,k,some", [(1500, 9000, 400, False), (4100, 4500, 400, False), (260, 17408, 400, False),
+                                        (65, 17408, 2064, False), (200, 9000, 2064, False), (260, 304, 8192, False),
+                                        (333, 5000, 4112, True), (1500, 9000, 400, True), (48, 9000, 784, True)])
+def test_fp8_linear_far_scales_plans(nv, m, n, k, some, kind):
+    xq, xs, wq, ws = far_scales(kind, m, n, k, 1250 + m + n + k)
+    if some:
+        near = np.arange(m) % 7 != 3
+        xs[near] *= np.float32(2.0 ** (-60 if kind == "above" else 60))
+        zero = [b for b in range(xs.shape[1]) if b % 3 == 2 or b >= 12]
+        xs[np.ix_(near, zero)] = 0
+    d = [dev(a) for a in (xq, xs, wq, ws)]
+    x, w = (decoded(d[i], d[i + 1].double(), block) for i, block in ((0, 1), (2, 128)))
+    ref = x.double() @ w.double().T          # all of one sign: also the sum of magnitudes
+    assert 2.0 ** -126 < float(ref.min()) and float(ref.max()) < 2.0 ** 127
+    for workspace in ("auto", None):
+        y = nv.fp8_linear(*d, workspace=workspace)
+        bad = ~((y.double() - ref).abs() <= F.linear_tolerance(1.0, 1.0, k) * ref)
+        assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} out of tolerance, first {bad.nonzero()[:3].tolist()}"
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["above", "below"])
 @pytest.mark.parametrize("t,topk,e,n,k", [(4, 2, 5, 130, 400), (300, 4, 6, 300, 1040)])
