@@ -453,9 +453,9 @@ nvfp4_status nvfp4_linear_w4a4(const uint16_t* x, int64_t m, int64_t n, int64_t 
                                int64_t workspace_bytes, void* stream);
 
 /*
- * E4M3 tensors with a scale per block.  Layers that a checkpoint keeps in 8
- * bits store OCP E4M3 codes and one FP32 scale per block of 1 x 128
- * (activations: one row, 128 consecutive k) or 128 x 128 (weights).  Layout of
+ * E4M3 tensors with a scale per block: OCP E4M3 codes and one FP32 scale per
+ * block of 1 x 128 (activations: one row, 128 consecutive k) or 128 x 128
+ * (weights), for layers that are kept in 8 bits.  Layout of
  * a rows x k tensor, k a multiple of 16 (the last block of either axis may be
  * short):
  *   codes  uint8 [rows, k]                                         row-major,

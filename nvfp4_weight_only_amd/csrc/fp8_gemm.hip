@@ -10,11 +10,11 @@
 // lane that scale the block's sum into the FP32 accumulators; those of one block
 // are issued two blocks later, while the matrix instructions run on.
 //
-// What bounds it: 2048 x 17408 x 5120 takes 190 us, 1.9 PFLOP/s (177 us if every
-// load found its line in L2; the matrix instructions and multiply-adds by
-// themselves 115 us, the LDS reads, 192 KB per chunk of 64 KB, 90 us); 4096^3 68 us,
-// 2.0 PFLOP/s.  With few rows of X the loads: 333 x 5000 x 17392 66 us, 58 if they
-// found their lines in L2; 64 x 5120 x 17408 30 us, 3.0 TB/s of W.
+// What bounds it: 2048 x 17408 x 5120 takes 184 us, 2.0 PFLOP/s (an earlier build 190,
+// 177 if every load found its line in L2; the matrix instructions and multiply-adds by
+// themselves 115 us, the LDS reads, 192 KB per chunk of 64 KB, 90 us); 4096^3 65 us,
+// 2.1 PFLOP/s.  With few rows of X the loads: 333 x 5000 x 17392 66 us, 58 if they
+// found their lines in L2; 64 x 5120 x 17408 29 us, 3.1 TB/s of W.
 //
 // LDS image of a chunk: row r (128 bytes) at 128 r, its 16-byte piece p at
 // piece p ^ (r & 7): a 128-bit read of one logical piece by 8 consecutive rows
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   } else {
     // Two scales, neither 0, whose product is no normal FP32 number: this wavefront's
     // sums again, block by block from memory, with the scales taken apart.  (So in the
-    // loop above, for every tile: 2048 x 17408 x 5120 198.5 us, 192.5 this way.)
+    // loop above, for every tile: 2048 x 17408 x 5120 198.5 us, 190.5 this way.)
     const uint8_t* xq = GROUPED ? p.xq : p.xq + m0 * p.k;
     const float* xs = GROUPED ? p.xs : p.xs + m0 * p.kb;
 #pragma unroll 1

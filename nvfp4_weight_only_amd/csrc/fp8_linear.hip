@@ -274,7 +274,8 @@ constexpr size_t kScalesLds = 65536;
 // and the sum of both bounds it.  A CU takes 43 ns per KB from HBM (6.1 TB/s over
 // the chip; a CU by itself is no faster, so shares have to be even) and 31 ns per
 // KB of X from L2, the lines in flight being what is scarce; a launch takes 1 us and
-// a workgroup's start and sums 3.  17408 x 5120 with M = 1, 16, 32, 48: 19.0, 21.2, 24.6 and 28.4 us.
+// a workgroup's start and sums 3.  17408 x 5120 with M = 1, 16, 32, 48: 19.6, 21.1,
+// 24.4 and 28.2 us.
 struct Skinny {
   int mt = 1;        // 16 mt rows of X per workgroup
   int64_t span = 0;  // rows of W per workgroup; 0: scales too long for LDS
@@ -312,7 +313,10 @@ bool skinny_supported(int64_t m, int64_t n, int64_t k) {
 
 // Measured, skinny against GEMM, us: M = 48 17408 x 5120 28.4 / 38.8, 5120 x 17408
 // 43.5 / 26.6; M = 96 5120 x 5120 21.8 / 18.1, 1024 x 2048 8.1 / 10.5; M = 200
-// 17408 x 128 13.3 / 6.4, 512 x 1024 5.4 / 6.5.
+// 17408 x 128 13.3 / 6.4, 512 x 1024 5.4 / 6.5.  Up to 16 rows the estimate is not
+// asked: M = 16 17408 x 5120 21.3 / 26.5, 5120 x 5120 10.7 / 12.9, 34816 x 5120 36.5 /
+// 47.6, 2048 x 8192 10.1 / 12.5, 1024 x 16384 15.3 / 15.8; but 5120 x 17408 26.9 / 23.6
+// (M = 8 22.9 / 23.0).
 // `split`: whether there is a workspace to split K with.
 static bool use_gemm(int64_t m, int64_t n, int64_t k, bool split) {
   if (!skinny_supported(m, n, k)) return true;
