@@ -10,6 +10,7 @@
 
 #include "device_common.hpp"
 #include "fp8_mfma.hpp"
+#include "fp8_tiles.hpp"
 #include "launch.hpp"
 
 namespace nvfp4 {
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_routed_kernel(SkinnyArgs p) {
 
 namespace {
 
-constexpr int kCus = 256, kMaxSpan = 80;
+using fp8_tiles::kCus;
+constexpr int kMaxSpan = 80;
 constexpr size_t kScalesLds = 65536;
 
 // Few rows of X: each CU streams its share of W through registers and reads all of X,

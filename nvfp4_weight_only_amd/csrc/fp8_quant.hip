@@ -450,7 +450,7 @@ static void launch_rows(const uint16_t* x, int64_t blocks, int64_t kb, int64_t k
   const dim3 grid((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22));
   if (kb >= 16 * U && k < ((int64_t)1 << 28))
     fp8_rows_kernel<SILU, U, true><<<grid, kThreads, 0, s>>>(x, blocks, (uint32_t)kb, k, codes, scales);
-  else
+  else if constexpr (U != 2)  // two blocks a thread only for kb of 32 to 63
     fp8_rows_kernel<SILU, U, false><<<grid, kThreads, 0, s>>>(x, blocks, (uint32_t)kb, k, codes, scales);
 }
 
