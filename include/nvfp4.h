@@ -509,7 +509,8 @@ nvfp4_status nvfp4_silu_mul_fp8(const uint16_t* gate_up, int64_t rows, int64_t n
  * places below it, so results are within 2^-10 of sum_k |x w| of the exact ones,
  * plus the BF16 output rounding, while the partial sums stay in FP32's normal range.
  * The scales may be of any size: a product xs * ws that is no normal FP32 number is
- * not formed (with more than about 64 rows of X, tiles with such scales take longer).
+ * not formed (with more than about 64 rows of X, tiles with such scales take up to 20
+ * times as long).
  * NaN codes and scales that are not finite reach the outputs of their row or column.
  * m = 0 is a no-op once n, k and the weight are valid (xq, xs and y may then be NULL).
  * Sizes beyond the launch's range are NVFP4_ERR_UNSUPPORTED.

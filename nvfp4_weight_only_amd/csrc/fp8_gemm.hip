@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_kernel(GemmArgs p) {
   } else {
     // Two scales, neither 0, whose product is no normal FP32 number: this wavefront's
     // sums again, block by block from memory, with the scales taken apart.  (So in the
-    // loop above, for every tile: 2048 x 17408 x 5120 198.5 us, 190.5 this way.)
+    // loop above, for every tile: 2048 x 17408 x 5120 198.5 us, 190.5 this way, and
+    // 3.1 ms where every tile has such scales.)
     const uint8_t* xq = GROUPED ? p.xq : p.xq + m0 * p.k;
     const float* xs = GROUPED ? p.xs : p.xs + m0 * p.kb;
 #pragma unroll 1
