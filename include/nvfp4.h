@@ -544,6 +544,139 @@ nvfp4_status nvfp4_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_
                                       const float* ws, uint16_t* y, void* workspace, int64_t workspace_bytes,
                                       void* stream);
 
+/*
+ * Operators around a paged FP4 cache of keys and values (layout: nvfp4_kv_gather):
+ * rotary positions, appending rows to the cache, attention that reads it.  The structs
+ * are host memory, read during the call; the pointers in them are device pointers.
+ *
+ * One layer's cache: codes and scales of keys and values, the same shape for both.
+ * format NVFP4_KV_NVFP4 (with a positive, finite FP32 tensor scale each) or
+ * NVFP4_KV_MXFP4 (k_tscale and v_tscale are ignored and may be NULL).
+ */
+typedef struct nvfp4_kv_cache {
+  int format;
+  int64_t num_blocks, block_size, heads, head_dim;
+  uint8_t* k_codes;  /* [num_blocks, block_size, heads, head_dim / 2] */
+  uint8_t* k_scales; /* [num_blocks, block_size, heads, head_dim / G] */
+  const float* k_tscale;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* v_tscale;
+} nvfp4_kv_cache;
+
+/*
+ * Rotary positions.  The first rot_dim elements of a head (a positive multiple of
+ * 16, at most head_dim) are turned: for i < rot_dim / 2 and the angle
+ * t = position * freqs[i] in radians (FP64), the pair (i, i + rot_dim / 2), or
+ * interleaved (2 i, 2 i + 1), becomes
+ *   amplitude * (x1 cos t - x2 sin t, x2 cos t + x1 sin t).
+ * Angles are good to FP64's precision up to 2^31 radians.
+ */
+typedef struct nvfp4_rope_spec {
+  const double* freqs; /* [rot_dim / 2] */
+  int64_t rot_dim;
+  float amplitude;
+  int interleaved;
+} nvfp4_rope_spec;
+
+/*
+ * nvfp4_rope: x [rows, heads, head_dim] -> out, both FP16 (NVFP4_OUT_F16) or BF16,
+ * row r at positions[r] (int32, any sign); the elements behind rot_dim are copied.
+ * Strides of rows and heads in elements, multiples of 8, not negative (heads of a
+ * merged projection, or heads outside rows); the last dimension is contiguous.
+ * Products in FP32, rounded once.  inverse turns by -t (with the same amplitude): it is
+ * the gradient of the rotation, and undoes one of amplitude 1.  out may be x with the
+ * same strides; otherwise they do not overlap, and out's rows and heads do not overlap
+ * each other (NVFP4_ERR_SHAPE).  head_dim a multiple of 8, at most 2048.  rows = 0 is a
+ * no-op.  x and out 16-byte aligned, freqs 8-byte, positions 4-byte aligned.
+ *
+ * nvfp4_rope_frequencies: freqs[i] (double) for i < rot_dim / 2, f = base^(-2 i / rot_dim),
+ * for contexts `factor` (at least 1) times as long as the `original` length:
+ *   NVFP4_ROPE_NONE        f
+ *   NVFP4_ROPE_LINEAR      f / factor
+ *   NVFP4_ROPE_BASE        f with base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *   NVFP4_ROPE_RAMP        f (1 - w) + w f / factor, w = (i - a) / (b - a) within [0, 1],
+ *                          a = floor(d(high)), b = ceil(d(low)) within [0, rot_dim - 1],
+ *                          d(n) = rot_dim log(original / (2 pi n)) / (2 log(base))
+ *   NVFP4_ROPE_WAVELENGTH  the same mean with w = (high - n) / (high - low) within [0, 1],
+ *                          n = original * f / (2 pi)
+ * Arguments that a scaling does not use are ignored; base <= 1, factor < 1 and bounds
+ * without 0 < low < high are NVFP4_ERR_UNSUPPORTED.
+ */
+#define NVFP4_ROPE_NONE 0
+#define NVFP4_ROPE_LINEAR 1
+#define NVFP4_ROPE_BASE 2
+#define NVFP4_ROPE_RAMP 3
+#define NVFP4_ROPE_WAVELENGTH 4
+
+nvfp4_status nvfp4_rope_frequencies(int scaling, int64_t rot_dim, double base, double factor, double original,
+                                    double low, double high, double* freqs, void* stream);
+nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads, int64_t head_dim,
+                        int64_t x_row_stride, int64_t x_head_stride, const int32_t* positions,
+                        const nvfp4_rope_spec* rope, int inverse, uint16_t* out, int64_t out_row_stride,
+                        int64_t out_head_stride, void* stream);
+
+/*
+ * A batch of sequences, for the two calls below: block_table [seqs, max_blocks] and
+ * seq_lens [seqs] as in nvfp4_kv_gather, row_start [seqs + 1], all int32 on the device.
+ * Rows row_start[s] .. row_start[s + 1] - 1 of the call are the LAST tokens of sequence
+ * s: row r is its token seq_lens[s] - (row_start[s + 1] - r), seq_lens counting them.
+ * row_start does not fall; NULL means one row a sequence (rows = seqs).  Rows before
+ * row_start[0] and from row_start[seqs] on belong to no sequence.  The device data is not
+ * validated on the host; whatever it holds, nothing outside the buffers is touched, and
+ * with a row_start that falls the results are unspecified.
+ *
+ * nvfp4_kv_append: k, v [rows, heads, head_dim] FP16 or BF16 -> their tokens' places in
+ * the cache.  With rope (NULL: none) keys are turned first, by positions[r] (int32 [rows],
+ * NULL: the token's index), in FP64, rounded to FP32 once.  Per block of G elements, ties
+ * to the even code, on exact quotients:
+ *   NVFP4  scale = E4M3 nearest to amax / (6 tscale), at most 448;
+ *          code = sign | E2M1 magnitude nearest to |x| / (scale tscale), at most 6
+ *          (magnitude 0 if scale is 0);
+ *   MXFP4  as nvfp4_mx_quantize.
+ * A block with a value that is not finite gets a NaN scale (0x7F, 0xFF) and codes 0.
+ * Rows of no sequence, tokens below 0, from max_blocks * block_size on or in a page outside
+ * [0, num_blocks) are skipped; the rest of the cache keeps its contents.  Two rows of a
+ * call with the same place (sequences that share a page they both append to) leave it
+ * unspecified.  head_dim at most 2048.
+ *
+ * nvfp4_kv_attention: q [rows, q_heads, head_dim] -> out [rows, q_heads, head_dim]
+ * (contiguous, the same type): query head h reads key/value head h / (q_heads / heads).
+ * A row at token p of its sequence sees the tokens t <= p, and t > p - window if
+ * window > 0, that are below min(seq_lens[s], max_blocks * block_size) and in a page inside
+ * [0, num_blocks):
+ *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t),
+ * k_t and v_t = E2M1 * scale (* tscale), scores, maxima and sums in FP32, rounded once.
+ * A row that sees nothing gives zeros; rows of no sequence are left as they were.  Tokens
+ * that a row does not see do not touch it, whatever the cache holds there.  Products run on
+ * the matrix cores in 16 bits: codes times their block scales are exact there, the
+ * query is (or is off by less than 2^-25 of its row's largest element), the weights w_t are
+ * rounded to 11 significant bits (to 2^-32 of the largest where that is more), with MXFP4 to 8
+ * bits for BF16 outputs and 15 for FP16 ones.
+ * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
+ * rows * q_heads < 2^31 (others NVFP4_ERR_UNSUPPORTED).
+ * Workspace: nvfp4_kv_attention_workspace_bytes bytes (-1: invalid or unsupported shape; no
+ * HIP call), any contents, overlapping no argument, not shared by calls in flight at the same
+ * time; NULL is NVFP4_ERR_NULL, fewer bytes NVFP4_ERR_SHAPE.
+ *
+ * Common errors: as nvfp4_kv_gather; q_heads not a multiple of heads is NVFP4_ERR_SHAPE;
+ * max_blocks * block_size above 2^31 - 4097 NVFP4_ERR_UNSUPPORTED; codes, scales, k, v, q,
+ * out and workspace 16-byte aligned, strides as in nvfp4_rope.  rows = 0 or seqs = 0 is a
+ * no-op.
+ */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, int type, const uint16_t* k, const uint16_t* v, int64_t rows,
+                             int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                             const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                             const int32_t* row_start, int64_t seqs, const nvfp4_rope_spec* rope,
+                             const int32_t* positions, void* stream);
+int64_t nvfp4_kv_attention_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
+                                           int64_t seqs);
+nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int type, const uint16_t* q, int64_t rows,
+                                int64_t q_heads, int64_t q_row_stride, int64_t q_head_stride,
+                                const int32_t* block_table, int64_t max_blocks, const int32_t* seq_lens,
+                                const int32_t* row_start, int64_t seqs, float scale, int64_t window, uint16_t* out,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

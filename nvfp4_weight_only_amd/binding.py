@@ -33,7 +33,20 @@ EXPORTED = ("nvfp4_status_string", "nvfp4_version", "nvfp4_quantize", "nvfp4_ama
             "nvfp4_stream_read", "nvfp4_stream_read_sink_words", "nvfp4_quantize_ws",
             "nvfp4_quantize_workspace_bytes", "nvfp4_fp8_quantize", "nvfp4_rmsnorm_fp8", "nvfp4_silu_mul_fp8",
             "nvfp4_fp8_linear_workspace_bytes", "nvfp4_fp8_linear", "nvfp4_fp8_linear_grouped_workspace_bytes",
-            "nvfp4_fp8_linear_grouped")
+            "nvfp4_fp8_linear_grouped", "nvfp4_rope_frequencies", "nvfp4_rope", "nvfp4_kv_append",
+            "nvfp4_kv_attention_workspace_bytes", "nvfp4_kv_attention")
+
+
+class _KvCacheStruct(ctypes.Structure):  # nvfp4_kv_cache
+    _fields_ = [("format", ctypes.c_int), ("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("k_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("k_tscale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("v_tscale", ctypes.c_void_p)]
+
+
+class _RopeStruct(ctypes.Structure):  # nvfp4_rope_spec
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int64), ("amplitude", ctypes.c_float),
+                ("interleaved", ctypes.c_int)]
 
 
 class NVFP4Error(RuntimeError):
@@ -98,6 +111,13 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_fp8_linear.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
         L.nvfp4_fp8_linear_grouped_workspace_bytes.argtypes = [i64, i64, i64]
         L.nvfp4_fp8_linear_grouped.argtypes = [vp, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+        f64 = ctypes.c_double
+        L.nvfp4_rope_frequencies.argtypes = [i32, i64, f64, f64, f64, f64, f64, vp, vp]
+        L.nvfp4_rope.argtypes = [i32, vp, i64, i64, i64, i64, i64, vp, vp, i32, vp, i64, i64, vp]
+        L.nvfp4_kv_append.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, vp]
+        L.nvfp4_kv_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+        L.nvfp4_kv_attention.argtypes = [vp, i32, vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, ctypes.c_float, i64, vp,
+                                         vp, i64, vp]
         for name in EXPORTED[2:]:
             getattr(L, name).restype = i64 if name.endswith(("_workspace_bytes", "_max_bytes", "_prepared_bytes", "_sink_words")) \
                 else i32
@@ -819,4 +839,232 @@ def fp8_linear_grouped(xq: torch.Tensor, xs: torch.Tensor, route: torch.Tensor, 
     _call(lib().nvfp4_fp8_linear_grouped, "nvfp4_fp8_linear_grouped", device, xq.data_ptr(), xs.data_ptr(), t, topk,
           route.data_ptr(), e, n, k, wq.data_ptr(), ws.data_ptr(), out.data_ptr(), workspace.data_ptr(),
           workspace.numel())
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around a paged FP4 cache of keys and values.
+# ---------------------------------------------------------------------------
+_HALF_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+_ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3, "wavelength": 4}
+
+
+def _need_heads(t: torch.Tensor, name: str) -> int:
+    """The type code of a [rows, heads, head_dim] tensor of FP16 or BF16 whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    code = _HALF_TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim]")
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return code
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_length: float = 0.0, low: float = 1.0, high: float = 32.0,
+                     device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    """Angular frequencies of rotary positions, float64 [rot_dim / 2]: base^(-2 i / rot_dim), changed for contexts
+    `factor` times as long as original_length.
+
+    scaling: None; "linear" (positions interpolated); "base" (a larger base: the slowest frequency slowed by the
+    factor, the fastest kept); "ramp" (frequencies whose wavelength fits original_length more than `high` times kept,
+    those below `low` times slowed by the factor, linearly over the index in between) or "wavelength" (the same bounds,
+    linearly over the number of turns).  Some long-context models also scale the turned values, ramp ones by
+    0.1 log(factor) + 1: that is Rope's amplitude."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if rot_dim <= 0 or rot_dim % 16 != 0:
+        raise ValueError(f"rot_dim must be a positive multiple of 16, got {rot_dim}")
+    freqs = torch.empty(rot_dim // 2, dtype=torch.float64, device=device)
+    if not freqs.is_cuda:
+        raise ValueError("device must be a GPU")
+    _call(lib().nvfp4_rope_frequencies, "nvfp4_rope_frequencies", freqs.device, _ROPE_SCALINGS[scaling], rot_dim, base,
+          factor, original_length, low, high, freqs.data_ptr())
+    return freqs
+
+
+class Rope:
+    """A position rotation, made once and kept: the first 2 * len(freqs) elements of a head turned by position * freqs
+    (float64, radians a token, on the device), pairs (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved, times
+    amplitude."""
+
+    def __init__(self, freqs: torch.Tensor, amplitude: float = 1.0, interleaved: bool = False):
+        _need(freqs, torch.float64, "freqs")
+        if freqs.dim() != 1 or freqs.numel() == 0 or freqs.numel() % 8 != 0:
+            raise ValueError("freqs must be [rot / 2], rot a positive multiple of 16")
+        self.freqs, self.amplitude, self.interleaved = freqs, float(amplitude), bool(interleaved)
+        self.rot_dim = 2 * freqs.numel()
+        self._struct = _RopeStruct(freqs.data_ptr(), self.rot_dim, self.amplitude, int(self.interleaved))
+        self._ref = ctypes.addressof(self._struct)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: Optional[torch.Tensor] = None,
+         inverse: bool = False) -> torch.Tensor:
+    """x [rows, heads, head_dim] (FP16 or BF16; any strides of rows and heads that are multiples of 8) turned by
+    positions [rows] (int32).  out: x itself (in place) or a tensor of its shape and type; a contiguous one is
+    allocated when it is not given.  inverse turns back: the rotation's gradient."""
+    code = _need_heads(x, "x")
+    _need(positions, torch.int32, "positions")
+    rows, heads, head_dim = x.shape
+    if positions.shape != (rows,):
+        raise ValueError("positions must be [rows]")
+    if rope.rot_dim > head_dim:
+        raise ValueError(f"the rotation turns {rope.rot_dim} elements, a head has {head_dim}")
+    if out is not None:
+        if _need_heads(out, "out") != code or out.shape != x.shape:
+            raise ValueError("out must have x's shape and type")
+    device = _one_device(x, positions, rope.freqs, out)
+    if out is None:
+        out = torch.empty((rows, heads, head_dim), dtype=x.dtype, device=device)
+    _call(lib().nvfp4_rope, "nvfp4_rope", device, code, x.data_ptr(), rows, heads, head_dim, x.stride(0), x.stride(1),
+          positions.data_ptr(), rope._ref, int(inverse), out.data_ptr(), out.stride(0), out.stride(1))
+    return out
+
+
+class KVCache:
+    """One layer's keys and values in a paged FP4 cache, made once and kept: the tensors that kv_gather takes (codes
+    uint8 [num_blocks, block_size, heads, head_dim/2], scales uint8 [..., head_dim/G]; tensor scales float32 [1] for
+    "nvfp4", none for "mxfp4"), for kv_append and kv_attention."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 k_tscale: Optional[torch.Tensor] = None, v_tscale: Optional[torch.Tensor] = None, fmt: str = "nvfp4"):
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"unknown KV format {fmt!r}")
+        for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+            _need(t, torch.uint8, name)
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [num_blocks, block_size, heads, *]")
+        nb, bs, heads, half = k_codes.shape
+        if half == 0 or 2 * half % _KV_GROUP[fmt] != 0:
+            raise ValueError(f"head_dim must be a positive multiple of {_KV_GROUP[fmt]}")
+        if v_codes.shape != k_codes.shape:
+            raise ValueError("v_codes must have k_codes' shape")
+        if k_scales.shape != (nb, bs, heads, 2 * half // _KV_GROUP[fmt]) or v_scales.shape != k_scales.shape:
+            raise ValueError("scales do not match codes")
+        if fmt == "nvfp4":
+            for t, name in ((k_tscale, "k_tscale"), (v_tscale, "v_tscale")):
+                if t is None:
+                    raise ValueError(f"an NVFP4 cache needs {name}")
+                _need(t, torch.float32, name)
+                if t.numel() != 1:
+                    raise ValueError(f"{name} must be [1]")
+        else:
+            k_tscale = v_tscale = None
+        self.device = _one_device(k_codes, k_scales, v_codes, v_scales, k_tscale, v_tscale)
+        self.k_codes, self.k_scales, self.k_tscale = k_codes, k_scales, k_tscale
+        self.v_codes, self.v_scales, self.v_tscale = v_codes, v_scales, v_tscale
+        self.fmt, self.num_blocks, self.block_size, self.heads, self.head_dim = fmt, nb, bs, heads, 2 * half
+        self._struct = _KvCacheStruct(KV_FORMATS[fmt], nb, bs, heads, 2 * half, k_codes.data_ptr(), k_scales.data_ptr(),
+                                      None if k_tscale is None else k_tscale.data_ptr(), v_codes.data_ptr(),
+                                      v_scales.data_ptr(), None if v_tscale is None else v_tscale.data_ptr())
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def zeros(cls, num_blocks: int, block_size: int, heads: int, head_dim: int, fmt: str = "nvfp4",
+              k_tscale: Optional[torch.Tensor] = None, v_tscale: Optional[torch.Tensor] = None,
+              device: Union[str, torch.device] = "cuda") -> "KVCache":
+        """A new cache whose values are all 0."""
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"unknown KV format {fmt!r}")
+        shape = (num_blocks, block_size, heads)
+        k_codes, v_codes = (torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2))
+        k_scales, v_scales = (torch.zeros((*shape, head_dim // _KV_GROUP[fmt]), dtype=torch.uint8, device=device)
+                              for _ in range(2))
+        return cls(k_codes, k_scales, v_codes, v_scales, k_tscale, v_tscale, fmt)
+
+
+def _batch(cache: KVCache, rows: int, block_table: torch.Tensor, seq_lens: torch.Tensor,
+           row_start: Optional[torch.Tensor]) -> Tuple:
+    """The C entry points' batch arguments."""
+    _need(block_table, torch.int32, "block_table")
+    _need(seq_lens, torch.int32, "seq_lens")
+    if block_table.dim() != 2 or seq_lens.shape != (block_table.shape[0],):
+        raise ValueError("block_table must be [seqs, max_blocks] and seq_lens [seqs]")
+    seqs = block_table.shape[0]
+    if row_start is None:
+        if rows != seqs:
+            raise ValueError("without row_start every sequence has one row")
+    else:
+        _need(row_start, torch.int32, "row_start")
+        if row_start.shape != (seqs + 1,):
+            raise ValueError("row_start must be [seqs + 1]")
+    return (block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+            None if row_start is None else row_start.data_ptr(), seqs)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+              row_start: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+              positions: Optional[torch.Tensor] = None) -> None:
+    """Write keys and values (FP16 or BF16 [rows, heads, head_dim], strides as for rope()) into the cache in place.
+
+    block_table int32 [seqs, max_blocks], seq_lens int32 [seqs] (the tokens in the cache after the call), row_start
+    int32 [seqs + 1]: rows row_start[s] .. row_start[s + 1] are the last tokens of sequence s (None: one row each).
+    With `rope` the keys are turned first, by positions (int32 [rows]) or their tokens' indices."""
+    code = _need_heads(k, "k")
+    if _need_heads(v, "v") != code:
+        raise ValueError("k and v must have the same type")
+    rows = k.shape[0]
+    if k.shape[1:] != (cache.heads, cache.head_dim) or v.shape != k.shape:
+        raise ValueError("k and v must be [rows, heads, head_dim] of the cache")
+    batch = _batch(cache, rows, block_table, seq_lens, row_start)
+    if rope is not None and rope.rot_dim > cache.head_dim:
+        raise ValueError(f"the rotation turns {rope.rot_dim} elements, a head has {cache.head_dim}")
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions need a rope")
+        _need(positions, torch.int32, "positions")
+        if positions.shape != (rows,):
+            raise ValueError("positions must be [rows]")
+    device = _one_device(cache.k_codes, k, v, block_table, seq_lens, row_start, positions,
+                         None if rope is None else rope.freqs)
+    _call(lib().nvfp4_kv_append, "nvfp4_kv_append", device, cache._ref, code, k.data_ptr(), v.data_ptr(), rows,
+          k.stride(0), k.stride(1), v.stride(0), v.stride(1), *batch, None if rope is None else rope._ref,
+          None if positions is None else positions.data_ptr())
+
+
+def kv_attention_workspace_bytes(heads: int, head_dim: int, q_heads: int, rows: int, seqs: int) -> int:
+    """Workspace bytes nvfp4_kv_attention needs."""
+    b = lib().nvfp4_kv_attention_workspace_bytes(heads, head_dim, q_heads, rows, seqs)
+    if b < 0:
+        raise ValueError(f"no attention for heads={heads} head_dim={head_dim} q_heads={q_heads} rows={rows} seqs={seqs}")
+    return b
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 row_start: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 window: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of q (FP16 or BF16 [rows, q_heads, head_dim], strides as for rope(); q_heads a multiple of the cache's
+    heads) to the cache: each row, the batch's arguments as in kv_append, sees its sequence's tokens up to its own,
+    the last `window` of them if one is given.  scale: head_dim ** -0.5 if it is not given.
+
+    out: a contiguous tensor of q's shape and type; rows of no sequence are left as they were in it.  workspace: a
+    uint8 device tensor of at least kv_attention_workspace_bytes(...) bytes; allocated when it is not given."""
+    code = _need_heads(q, "q")
+    rows, q_heads, head_dim = q.shape
+    if head_dim != cache.head_dim or q_heads == 0 or q_heads % cache.heads != 0:
+        raise ValueError("q must be [rows, q_heads, head_dim], q_heads a multiple of the cache's heads")
+    batch = _batch(cache, rows, block_table, seq_lens, row_start)
+    if window is None:
+        window = 0
+    elif window <= 0:
+        raise ValueError("window must be positive")
+    if out is not None:
+        _need(out, q.dtype, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    need = kv_attention_workspace_bytes(cache.heads, head_dim, q_heads, rows, batch[-1])
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    device = _one_device(cache.k_codes, q, block_table, seq_lens, row_start, out, workspace)
+    if out is None:
+        out = torch.empty((rows, q_heads, head_dim), dtype=q.dtype, device=device)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(lib().nvfp4_kv_attention, "nvfp4_kv_attention", device, cache._ref, code, q.data_ptr(), rows, q_heads,
+          q.stride(0), q.stride(1), *batch, head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return out

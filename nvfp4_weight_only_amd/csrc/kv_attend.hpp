@@ -1,0 +1,224 @@
+// The parts of attention over a paged FP4 cache that its kernels share: arguments,
+// the loads and the decoding of cache rows, the partial results and their join.
+//
+// For a row at position p of its sequence and a query head with key/value head h,
+//   o = tscale_v sum_t w_t v_t / sum_t w_t,  w_t = exp(scale tscale_k q . k_t),
+// over the tokens t <= p (and t > p - window) that are in the cache, k and v without
+// their tensor scales.  The sums run over tiles of tokens with the running maximum m,
+// the sum l of 2^(s - m) and the unnormalized output, all in FP32; parts of the tokens
+// that different wavefronts or workgroups took are joined by their m, l and output.
+//
+// What the matrix cores multiply.  NVFP4: E2M1 * E4M3 has at most 6 significant bits
+// and lies in [2^-10, 2688], so keys and values are exact in FP16, where a pair of
+// codes takes one conversion and one packed product.  The query's row is divided by the
+// power of two of its largest element, so that any BF16 or FP16 row fits FP16 (what
+// lies 2^14 below the largest loses bits, less than 2^-25 of the largest); weights are
+// rounded to FP16.  MXFP4: E2M1 * 2^(byte - 127) needs BF16's range and is exact there,
+// in one conversion a pair.  A BF16 query is exact too, and weights are rounded to
+// BF16, half a step of the output's type; for FP16 queries and outputs the query (exactly)
+// and the weights (to 16 bits) are split into two BF16 terms each.
+#pragma once
+
+#include "kv_common.hpp"
+
+namespace nvfp4 {
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef short i16x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Weights are 2^(s - m + bias) with m at most kSlack (log2 units) below the running
+// maximum, so up to 2^15, FP16's last power of two: one 2^21 below the largest is still a
+// normal FP16 number, and below that it is off by at most 2^-32 of the largest (without
+// the bias by 2^-25, which 10^5 small weights add up to something seen).  Sums keep the
+// bias; it cancels in the quotient.
+constexpr float kSlack = 8.0f, kWeightBias = 7.0f;
+
+struct AttendArgs {
+  KvCache c;
+  KvBatch b;
+  FastDiv page, group;
+  int64_t cap;  // max_blocks * block_size
+  const uint16_t* q;
+  int64_t q_row, q_head;
+  uint16_t* out;  // [rows, q_heads, head_dim]
+  int32_t q_heads, g;  // g = q_heads / heads
+  float scale;
+  int32_t window;  // 0: none
+  int32_t hw, tw, hgroups;  // heads and token slices of a workgroup, groups of heads
+  int32_t nwg;              // workgroups of a group of heads
+  float* part;              // partial results
+  int64_t* prefix;          // [seqs + 1] units before each sequence
+};
+
+// 16-bit matrix type and splits by format and query type.
+template <bool MX, bool BF16>
+struct AttendTypes {
+  static constexpr int kTerms = MX && !BF16 ? 2 : 1;
+};
+
+// D = A B + C on 16 x 16 x 32 (A: 16 tokens or dims; B: 16 rows of queries).
+template <bool MX>
+__device__ __forceinline__ f32x4_t mfma16(const u32x4v_t& a, const u32x4v_t& b, const f32x4_t& c) {
+  if constexpr (MX)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// Two floats as the matrix type.
+template <bool MX>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return f32x2_to_half<MX>(a, b);
+}
+// What the first term left out, as the matrix type (BF16).
+__device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t first) {
+  return f32x2_to_half<true>(a - bf16_to_f32(first & 0xFFFFu), b - __uint_as_float(first & 0xFFFF0000u));
+}
+
+// Scale bytes that a lane needs of a row whose quarter (NS pieces of 8 elements) it holds, and where they are.
+template <bool MX, int NS>
+struct ScaleBytes {
+  static constexpr int kRow = MX ? NS : 2 * NS;  // bytes of a row: head_dim = 32 NS
+  static constexpr int kShift = MX ? 2 : 1;      // log2 pieces a block
+  // Blocks that NS pieces from quarter * NS on touch at most.
+  static constexpr int kLoad = MX ? (NS <= 2 || NS == 4 ? 1 : 2) : (NS == 3 ? 2 : NS / 2);
+  static __device__ __forceinline__ int base(int quarter) {
+    const int b = (quarter * NS) >> kShift;
+    return b + kLoad > kRow ? kRow - kLoad : b;
+  }
+  // Byte of piece c in the loaded word.
+  static __device__ __forceinline__ int index(int quarter, int c) {
+    if constexpr ((NS * 1) % (1 << kShift) == 0 || (MX && NS == 2)) return MX && NS == 2 ? 0 : c >> kShift;
+    else return ((quarter * NS + c) >> kShift) - base(quarter);
+  }
+  static __device__ __forceinline__ uint32_t load(const uint8_t* p) {
+    if constexpr (kLoad == 1) return *p;
+    if constexpr (kLoad == 2) return (uint32_t)p[0] | (uint32_t)p[1] << 8;
+    if constexpr (kLoad == 3) return (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
+    return *reinterpret_cast<const uint32_t*>(p);
+  }
+};
+// With an even number of bytes the row's offset is even, and the load is one.
+template <>
+__device__ __forceinline__ uint32_t ScaleBytes<false, 4>::load(const uint8_t* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+template <>
+__device__ __forceinline__ uint32_t ScaleBytes<true, 8>::load(const uint8_t* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+
+// Whether a block with this scale byte can hold values that are not finite.
+template <bool MX>
+__device__ __forceinline__ bool scale_nonfinite(uint32_t word, int bytes) {
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (word >> (8 * i)) & 0xFFu;
+    r |= i < bytes && (MX ? b >= 253u : (b & 0x7Fu) == 0x7Fu);
+  }
+  return r;
+}
+
+// 8 codes times their block's scale in the matrix type, natural order.
+__device__ __forceinline__ u32x4v_t decode8_nv(uint32_t w, f16x2_t s) {
+  const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s;
+  const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s;
+  const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s;
+  const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s;
+  return u32x4v_t{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                  __builtin_bit_cast(uint32_t, d)};
+}
+// The conversion multiplies by the scale's exponent alone: byte 0 is 2^-127, 255 NaN.
+__device__ __forceinline__ u32x4v_t decode8_mx(uint32_t w, float s) {
+  return u32x4v_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+}
+
+// A lane's quarter of a cache row: NS pieces of 8.
+template <bool MX, int NS>
+__device__ __forceinline__ void decode_quarter(const uint32_t (&w)[NS], uint32_t sw, int quarter, u32x4v_t (&out)[NS]) {
+  using B = ScaleBytes<MX, NS>;
+  if constexpr (MX) {
+#pragma unroll
+    for (int c = 0; c < NS; ++c)
+      out[c] = decode8_mx(w[c], __uint_as_float(((sw >> (8 * B::index(quarter, c))) & 0xFFu) << 23));
+  } else {
+    const f16x2_t s01 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, false);
+    f16x2_t s23 = s01;
+    if constexpr (B::kLoad > 2) s23 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, true);
+#pragma unroll
+    for (int c = 0; c < NS; ++c) {
+      const int i = B::index(quarter, c);
+      const f16x2_t pair = i >= 2 ? s23 : s01;
+      const _Float16 s = i & 1 ? pair[1] : pair[0];
+      out[c] = decode8_nv(w[c], f16x2_t{s, s});
+    }
+  }
+}
+
+// A row of queries' scale: s = factor * (the product of the matrix type's values) in
+// units of log2; the query's elements times `mul`.
+struct RowScale {
+  float factor, mul;
+};
+template <bool MX>
+__device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts) {
+  const float c = scale * ts * kLog2e;
+  RowScale r;
+  r.factor = fabsf(c);
+  r.mul = c < 0.0f ? -1.0f : 1.0f;
+  if constexpr (!MX) {
+    const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
+    if (amax > 0.0f && e != 255u) {
+      const int n = (int)e - 127;  // FP32 subnormals (e = 0) by 2^-127
+      r.factor = __builtin_amdgcn_ldexpf(r.factor, n);
+      r.mul = __builtin_amdgcn_ldexpf(r.mul, -n);
+    }
+  }
+  return r;
+}
+
+// Units (tiles of tokens times tiles of rows) that a sequence takes.
+struct SeqWork {
+  SeqRows r;
+  int64_t lo, hi;  // tokens that some row sees: lo a multiple of 32
+  int64_t rtiles, ttiles;
+};
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int64_t s, int rows_tile, int tokens_tile) {
+  SeqWork w;
+  w.r = seq_rows(a.b, a.cap, s);
+  w.lo = 0;
+  w.hi = 0;
+  w.rtiles = 0;
+  w.ttiles = 0;
+  if (w.r.count == 0) return w;
+  const int64_t p0 = w.r.first + w.r.shift, p1 = p0 + w.r.count - 1;
+  w.hi = w.r.len < p1 + 1 ? w.r.len : p1 + 1;
+  w.lo = a.window > 0 && p0 - a.window + 1 > 0 ? (p0 - a.window + 1) & ~(int64_t)31 : 0;
+  w.rtiles = (w.r.count * a.g + rows_tile - 1) / rows_tile;
+  // A sequence whose rows see nothing still has its zeros to write.
+  w.ttiles = w.hi > w.lo ? (w.hi - w.lo + tokens_tile - 1) / tokens_tile : 1;
+  return w;
+}
+
+// Workgroups that share `total` units: workgroup w of them takes units
+// w total / n up to (w + 1) total / n.
+__device__ __forceinline__ int64_t sharing(const AttendArgs& a, int64_t total) { return total < a.nwg ? total : a.nwg; }
+
+// 4 outputs of a row.
+template <bool BF16>
+__device__ __forceinline__ void store_out4(uint16_t* p, const f32x4_t& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(f32x2_to_half<BF16>(v[0], v[1]), f32x2_to_half<BF16>(v[2], v[3]));
+}
+
+}  // namespace nvfp4

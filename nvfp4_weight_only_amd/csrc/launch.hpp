@@ -170,6 +170,23 @@ void launch_fp8_linear_grouped(const uint8_t* xq, const float* xs, int64_t t_cou
                                int64_t experts, int64_t n, int64_t k, const uint8_t* wq, const float* ws, uint16_t* y,
                                void* workspace, hipStream_t s);
 
+// The operators around a paged FP4 cache of keys and values (kv_common.hpp); strides in elements, multiples of 8.
+struct KvCache;
+struct KvBatch;
+struct RopeArgs;
+void launch_rope(bool bf16, const uint16_t* x, int64_t rows, int64_t heads, int64_t head_dim, int64_t x_row,
+                 int64_t x_head, const int32_t* positions, const RopeArgs& rope, bool inverse, uint16_t* out,
+                 int64_t out_row, int64_t out_head, hipStream_t s);
+void launch_rope_frequencies(int scaling, int64_t rot, double base, double factor, double original, double low,
+                             double high, double* freqs, hipStream_t s);
+void launch_kv_append(const KvCache& c, const KvBatch& b, bool bf16, const uint16_t* k, const uint16_t* v,
+                      int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head, const RopeArgs& rope,
+                      const int32_t* positions, hipStream_t s);
+// head_dim 64, 96, 128, 192 or 256; rows * q_heads < 2^31.
+int64_t kv_attend_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs);
+void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint16_t* q, int64_t q_heads, int64_t q_row,
+                      int64_t q_head, float scale, int64_t window, uint16_t* out, void* workspace, hipStream_t s);
+
 // Plain streaming read of `bytes` bytes (a multiple of 16) of device memory by
 // stream_read_blocks(bytes) <= kStreamSinkWords workgroups; workgroup b stores the
 // XOR of the 32-bit words it read to sink[b].
