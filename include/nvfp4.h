@@ -646,7 +646,8 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * window > 0, that are below min(seq_lens[s], max_blocks * block_size) and in a page inside
  * [0, num_blocks):
  *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t),
- * k_t and v_t = E2M1 * scale (* tscale), scores, maxima and sums in FP32, rounded once.
+ * k_t and v_t = E2M1 * scale (* tscale; an MXFP4 block whose byte is 253 or 254, where 6 *
+ * 2^(byte - 127) passes FP32's range, counts as NaN as one of 255 does), scores, maxima and sums in FP32, rounded once.
  * A row that sees nothing gives zeros; rows of no sequence are left as they were.  Tokens
  * that a row does not see do not touch it, whatever the cache holds there.  Products run on
  * the matrix cores in 16 bits: codes times their block scales are exact there, the
@@ -654,7 +655,8 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * rounded to 11 significant bits (to 2^-32 of the largest where that is more), with MXFP4 to 8
  * bits for BF16 outputs and 15 for FP16 ones.
  * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
- * rows * q_heads < 2^31 (others NVFP4_ERR_UNSUPPORTED).
+ * rows * q_heads < 2^31, and num_blocks * block_size * heads at most 2^30 (others
+ * NVFP4_ERR_UNSUPPORTED).
  * Workspace: nvfp4_kv_attention_workspace_bytes bytes (-1: invalid or unsupported shape; no
  * HIP call), any contents, overlapping no argument, not shared by calls in flight at the same
  * time; NULL is NVFP4_ERR_NULL, fewer bytes NVFP4_ERR_SHAPE.

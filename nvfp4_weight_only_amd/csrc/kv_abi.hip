@@ -17,6 +17,8 @@ constexpr int64_t kMaxRow = (int64_t)1 << 24;    // elements of a row of heads
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxTokens = INT32_MAX - 4096;  // tokens of a sequence: a tile's end stays an int32
 
+constexpr int64_t kMaxCacheRows = (int64_t)1 << 30;  // tokens times heads that attention addresses
+
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct Range {
@@ -222,7 +224,8 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int type, const uin
   nvfp4::KvBatch b;
   if ((st = check_batch(c, rows, block_table, max_blocks, seq_lens, row_start, seqs, &b)) != NVFP4_OK) return st;
   if (q_heads <= 0 || q_heads % c.heads != 0 || window < 0 || workspace_bytes < 0) return NVFP4_ERR_SHAPE;
-  if (!attention_head_dim(c.head_dim) || q_heads > UINT16_MAX || rows > kMaxRows / q_heads)
+  if (!attention_head_dim(c.head_dim) || q_heads > UINT16_MAX || rows > kMaxRows / q_heads ||
+      c.num_blocks * c.block_size * c.heads > kMaxCacheRows)
     return NVFP4_ERR_UNSUPPORTED;
   int64_t qb;
   if ((st = extent(rows, q_heads, c.head_dim, &q_row_stride, &q_head_stride, &qb)) != NVFP4_OK) return st;

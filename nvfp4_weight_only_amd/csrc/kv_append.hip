@@ -116,19 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
   for (int i = wave; i < nrows; i += kAppendThreads / 64) {
     const int64_t r = r0 + i;
     int64_t s = r;
-    if (a.b.row_start) {
-      // 64 starts at a time; starts do not fall, so those at or before r come first.
-      int64_t lo = 0, hi = a.b.seqs;  // sequences lo .. hi - 1 may hold r
-      while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
-        const bool le = at < hi && (int64_t)a.b.row_start[at] <= r;
-        const int n = __popcll(__ballot(le));
-        if (n == 0) break;
-        lo += (int64_t)(n - 1) * step;
-        hi = lo + step < hi ? lo + step : hi;
-      }
-      s = lo;
-    }
+    if (a.b.row_start) s = find_sequence(a.b, r, lane);
     int64_t at = -1, t = -1;
     if (s < a.b.seqs) {
       const SeqRows q = seq_rows(a.b, a.cap, s);

@@ -14,7 +14,8 @@
 // power of two of its largest element, so that any BF16 or FP16 row fits FP16 (what
 // lies 2^14 below the largest loses bits, less than 2^-25 of the largest); weights are
 // rounded to FP16.  MXFP4: E2M1 * 2^(byte - 127) needs BF16's range and is exact there,
-// in one conversion a pair.  A BF16 query is exact too, and weights are rounded to
+// in one conversion a pair (bytes 253 and 254, whose blocks pass FP32's range, count as
+// NaN).  A BF16 query is exact too, and weights are rounded to
 // BF16, half a step of the output's type; for FP16 queries and outputs the query (exactly)
 // and the weights (to 16 bits) are split into two BF16 terms each.
 #pragma once
@@ -29,6 +30,9 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef short i16x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
+// MXFP4 scale bytes from here on count as NaN: 6 * 2^(253 - 127) is beyond FP32.
+constexpr uint32_t kMxNan = 253;
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Weights are 2^(s - m + bias) with m at most kSlack (log2 units) below the running
@@ -41,7 +45,7 @@ constexpr float kSlack = 8.0f, kWeightBias = 7.0f;
 struct AttendArgs {
   KvCache c;
   KvBatch b;
-  FastDiv page, group;
+  FastDiv page, group, unit;  // block_size, g, tokens of a unit
   int64_t cap;  // max_blocks * block_size
   const uint16_t* q;
   int64_t q_row, q_head;
@@ -72,6 +76,16 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4v_t& a, const u32x4v_t& b, 
                                                   0, 0);
 }
 
+// The same on 16 x 16 x 16.
+template <bool MX>
+__device__ __forceinline__ f32x4_t mfma16k16(const i16x4_t& a, const i16x4_t& b, const f32x4_t& c) {
+  typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+  if constexpr (MX) return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4_t, a), __builtin_bit_cast(f16x4_t, b), c, 0, 0,
+                                                 0);
+}
+
 // Two floats as the matrix type.
 template <bool MX>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -93,6 +107,8 @@ struct ScaleBytes {
     const int b = (quarter * NS) >> kShift;
     return b + kLoad > kRow ? kRow - kLoad : b;
   }
+  // Bytes of all quarters side by side: a quarter's start is at a multiple of kLoad.
+  static constexpr bool kEven = 4 * kLoad == kRow;
   // Byte of piece c in the loaded word.
   static __device__ __forceinline__ int index(int quarter, int c) {
     if constexpr ((NS * 1) % (1 << kShift) == 0 || (MX && NS == 2)) return MX && NS == 2 ? 0 : c >> kShift;
@@ -115,16 +131,19 @@ __device__ __forceinline__ uint32_t ScaleBytes<true, 8>::load(const uint8_t* p) 
   return *reinterpret_cast<const uint16_t*>(p);
 }
 
-// Whether a block with this scale byte can hold values that are not finite.
+// Whether a block with this scale byte holds values that are not finite.
 template <bool MX>
-__device__ __forceinline__ bool scale_nonfinite(uint32_t word, int bytes) {
-  bool r = false;
+__device__ __forceinline__ bool scale_nonfinite(uint32_t byte) {
+  return MX ? byte >= kMxNan : (byte & 0x7Fu) == 0x7Fu;
+}
+
+// The scale bytes with those of NaN blocks set to 0.
+template <bool MX>
+__device__ __forceinline__ uint32_t drop_nan(uint32_t word) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = (word >> (8 * i)) & 0xFFu;
-    r |= i < bytes && (MX ? b >= 253u : (b & 0x7Fu) == 0x7Fu);
-  }
-  return r;
+  for (int i = 0; i < 4; ++i)
+    if (scale_nonfinite<MX>((word >> (8 * i)) & 0xFFu)) word &= ~(0xFFu << (8 * i));
+  return word;
 }
 
 // 8 codes times their block's scale in the matrix type, natural order.
@@ -150,8 +169,10 @@ __device__ __forceinline__ void decode_quarter(const uint32_t (&w)[NS], uint32_t
   using B = ScaleBytes<MX, NS>;
   if constexpr (MX) {
 #pragma unroll
-    for (int c = 0; c < NS; ++c)
-      out[c] = decode8_mx(w[c], __uint_as_float(((sw >> (8 * B::index(quarter, c))) & 0xFFu) << 23));
+    for (int c = 0; c < NS; ++c) {
+      const uint32_t byte = (sw >> (8 * B::index(quarter, c))) & 0xFFu;
+      out[c] = decode8_mx(w[c], __uint_as_float((byte >= kMxNan ? 255u : byte) << 23));
+    }
   } else {
     const f16x2_t s01 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw, 1.0f, false);
     f16x2_t s23 = s01;
@@ -179,7 +200,7 @@ __device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts)
   r.mul = c < 0.0f ? -1.0f : 1.0f;
   if constexpr (!MX) {
     const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
-    if (amax > 0.0f && e != 255u) {
+    if (amax > 0.0f && e < 255u) {
       const int n = (int)e - 127;  // FP32 subnormals (e = 0) by 2^-127
       r.factor = __builtin_amdgcn_ldexpf(r.factor, n);
       r.mul = __builtin_amdgcn_ldexpf(r.mul, -n);
@@ -188,32 +209,34 @@ __device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts)
   return r;
 }
 
-// Units (tiles of tokens times tiles of rows) that a sequence takes.
+// What a sequence takes: tiles of rows times units of tokens.
 struct SeqWork {
-  SeqRows r;
-  int64_t lo, hi;  // tokens that some row sees: lo a multiple of 32
-  int64_t rtiles, ttiles;
+  int32_t first, packed;  // first row, rows times g
+  int32_t pos;            // token of the first row (negative: it sees nothing)
+  int32_t lo, hi;         // tokens that some row sees: lo a multiple of 32
+  int32_t rtiles, ttiles;
 };
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int64_t s, int rows_tile, int tokens_tile) {
+template <int ROWS>
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int32_t s) {
+  const SeqRows r = seq_rows(a.b, a.cap, s);
   SeqWork w;
-  w.r = seq_rows(a.b, a.cap, s);
-  w.lo = 0;
-  w.hi = 0;
-  w.rtiles = 0;
-  w.ttiles = 0;
-  if (w.r.count == 0) return w;
-  const int64_t p0 = w.r.first + w.r.shift, p1 = p0 + w.r.count - 1;
-  w.hi = w.r.len < p1 + 1 ? w.r.len : p1 + 1;
-  w.lo = a.window > 0 && p0 - a.window + 1 > 0 ? (p0 - a.window + 1) & ~(int64_t)31 : 0;
-  w.rtiles = (w.r.count * a.g + rows_tile - 1) / rows_tile;
+  w.first = (int32_t)r.first;
+  w.packed = (int32_t)r.count * a.g;
+  const int64_t p0 = r.first + r.shift, p1 = p0 + r.count;
+  w.pos = p0 < -a.b.rows ? -(int32_t)a.b.rows : (int32_t)p0;  // every row of such a sequence is below token 0
+  w.hi = (int32_t)(p1 < 0 ? 0 : (p1 < r.len ? p1 : r.len));
+  w.lo = a.window > 0 && p0 - a.window + 1 > 0 ? (int32_t)(p0 - a.window + 1) & ~31 : 0;
+  w.rtiles = (w.packed + ROWS - 1) / ROWS;
   // A sequence whose rows see nothing still has its zeros to write.
-  w.ttiles = w.hi > w.lo ? (w.hi - w.lo + tokens_tile - 1) / tokens_tile : 1;
+  w.ttiles = w.hi > w.lo ? fastdiv(w.hi - w.lo + a.unit.d - 1, a.unit) : 1;
   return w;
 }
 
-// Workgroups that share `total` units: workgroup w of them takes units
+// Workgroups that share `total` units: workgroup w of n takes units
 // w total / n up to (w + 1) total / n.
-__device__ __forceinline__ int64_t sharing(const AttendArgs& a, int64_t total) { return total < a.nwg ? total : a.nwg; }
+__device__ __forceinline__ int32_t sharing(const AttendArgs& a, int64_t total) {
+  return total < a.nwg ? (int32_t)total : a.nwg;
+}
 
 // 4 outputs of a row.
 template <bool BF16>

@@ -23,31 +23,34 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
 constexpr int kFewTokens = 32;
 
-// LDS of a wavefront: 32 tokens' values, rows 32 bytes longer than the values so that 8
-// rows start in different banks; at the end 16 rows of outputs, maximum and sum.
-template <int NS>
-struct FewLds {
-  static constexpr int kD = 32 * NS;
+// Sizes by head dimension, rows and terms.  One workgroup a CU, of 12 wavefronts where 168
+// registers do (16 would spill, and what a wavefront does once, some 800 instructions, counts
+// for each: 40 us for 16 streams of up to 8192 tokens instead of 32; 8 wavefronts 31, and one
+// stream of 131072 46 instead of 42), else 8.
+template <int NS, int RT, int TERMS>
+struct Few {
+  static constexpr int kD = 32 * NS, kRows = 16 * RT;
+  static constexpr int kWaves = NS <= 4 && RT == 1 ? 12 : 8;
+  static constexpr int kHeads = 4;  // of a workgroup, at most
+  static constexpr bool kQInLds = NS * RT * TERMS > 4;       // queries: more than 16 registers
+  // LDS: 16 tokens' values a wavefront, rows 32 bytes longer than the values, so that 8 rows start in different banks;
+  // the queries; at the end instead a wavefront's 16 rows of outputs with their maximum and sum.
   static constexpr int kRow = 2 * kD + 32;
+  static constexpr int kValues = 16 * kRow;
+  static constexpr int kQ = kQInLds ? RT * TERMS * NS * 1024 : 0;
   static constexpr int kOut = kD + 4;  // floats of an output row
   static constexpr int kStats = 16 * kOut * 4;
-  static constexpr int kBytes = (kFewTokens * kRow > kStats + 128 ? kFewTokens * kRow : kStats + 128);
-};
-
-// A tile's codes and scales as loaded: token lane % 16 (+ 16) of the tile, quarter lane / 16 of its row.
-template <int NS>
-struct FewTile {
-  uint32_t k[2][NS], v[2][NS];
-  uint32_t ks[2], vs[2];
-  uint32_t there[2];  // bit t: token t of the half tile is in the cache
+  static constexpr int kEnd = kStats + 128;
+  static constexpr int kLoop = kWaves * kValues + kHeads * kQ;
+  static constexpr int kLds = kLoop > kWaves * kEnd ? kLoop : kWaves * kEnd;
 };
 
 // Sum over the workgroup of one value a thread, and the sum of the threads before.
+template <int WAVES>
 __device__ __forceinline__ int64_t few_scan(int64_t v, int64_t* total) {
-  __shared__ int64_t wsum[kFewWaves];
+  __shared__ int64_t wsum[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t inc = v;
 #pragma unroll
@@ -59,7 +62,7 @@ __device__ __forceinline__ int64_t few_scan(int64_t v, int64_t* total) {
   __syncthreads();
   int64_t before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kFewWaves; ++i) {
+  for (int i = 0; i < WAVES; ++i) {
     before += i < wave ? wsum[i] : 0;
     all += wsum[i];
   }
@@ -69,187 +72,296 @@ __device__ __forceinline__ int64_t few_scan(int64_t v, int64_t* total) {
 }
 
 template <bool MX, bool BF16, int NS, int RT>
-__global__ void __launch_bounds__(kFewThreads) kv_attend_few_kernel(AttendArgs a) {
-  using L = FewLds<NS>;
+__global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerms>::kWaves))
+    kv_attend_few_kernel(AttendArgs a) {
+  constexpr int kTerms = AttendTypes<MX, BF16>::kTerms;
+  using F = Few<NS, RT, kTerms>;
   using SB = ScaleBytes<MX, NS>;
-  constexpr int kD = L::kD, kRows = 16 * RT, kTerms = AttendTypes<MX, BF16>::kTerms;
-  __shared__ __attribute__((aligned(16))) char lds[kFewWaves * L::kBytes];
-  __shared__ int64_t start[2];
+  constexpr int kWaves = F::kWaves, kThreads = 64 * kWaves, kD = F::kD, kRows = F::kRows;
+  constexpr int kAlign = NS % 4 == 0 ? 16 : (NS % 2 == 0 ? 8 : 4);  // of a quarter's codes
+  __shared__ __attribute__((aligned(16))) char lds[F::kLds];
+  __shared__ int64_t plan[4];  // first sequence, unit in it, first unit, end
+  __shared__ SeqWork first_work;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, quarter = lane >> 4;
-  const int hg = blockIdx.x % a.hgroups, wg = blockIdx.x / a.hgroups;
-  const int head = hg * a.hw + wave % a.hw, slice = wave / a.hw;
+  const int col = lane & 15, quarter = lane >> 4;    // row and quarter of its elements, in the products
+  const int ltok = lane >> 2, lquarter = lane & 3;  // token and quarter of its row, in the loads
+  const int turn = (4 * col + quarter) * 4;         // the lane that loaded what this one multiplies
+  const int wg = (int)blockIdx.x / a.hgroups, hg = (int)blockIdx.x - wg * a.hgroups;
+  const int slice = wave / a.hw, hh = wave - slice * a.hw, head = hg * a.hw + hh;
   const bool active = slice < a.tw && head < (int)a.c.heads;
-  const int tokens_tile = kFewTokens * a.tw;
 
-  // This workgroup's units.
-  int64_t total = 0, pre = 0, u = 0;
-  for (int64_t s0 = 0; s0 < a.b.seqs; s0 += kFewThreads) {
-    const int64_t s = s0 + tid;
-    u = 0;
-    if (s < a.b.seqs) {
-      const SeqWork w = seq_work(a, s, kRows, tokens_tile);
-      u = w.rtiles * w.ttiles;
-    }
-    int64_t chunk;
-    pre = total + few_scan(u, &chunk);
-    total += chunk;
-    if (blockIdx.x == 0 && s < a.b.seqs) a.prefix[s] = pre;
-  }
-  if (blockIdx.x == 0 && tid == 0) a.prefix[a.b.seqs] = total;
-  const int64_t nwg = sharing(a, total);
-  if (wg >= nwg) return;
-  int64_t cur = wg * total / nwg;
-  const int64_t end = (wg + 1) * total / nwg;
-  if (a.b.seqs <= kFewThreads) {
-    if (pre <= cur && cur < pre + u) {
-      start[0] = tid;
-      start[1] = cur - pre;
+  const float ts_k = MX ? 1.0f : *a.c.tscale[0], ts_v = MX ? 1.0f : *a.c.tscale[1];
+
+  // This workgroup's units: found by the first wavefront where 64 sequences are all there are (the others would only
+  // take issue slots from it), else by all.
+  if ((int32_t)a.b.seqs <= 64) {
+    if (wave == 0) {
+      int64_t u = 0;
+      SeqWork w;
+      if (lane < (int32_t)a.b.seqs) {
+        w = seq_work<kRows>(a, lane);
+        u = (int64_t)w.rtiles * w.ttiles;
+      }
+      int64_t inc = u;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int64_t up = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += up;
+      }
+      const int64_t pre = inc - u, total = __shfl(inc, 63, 64);
+      if (blockIdx.x == 0 && lane < (int32_t)a.b.seqs) a.prefix[lane] = pre;
+      if (blockIdx.x == 0 && lane == 0) a.prefix[a.b.seqs] = total;
+      const int nwg = sharing(a, total);
+      if (lane == 0) plan[2] = plan[3] = 0;
+      if (wg < nwg) {
+        const int64_t cur = div_i64(wg * total, nwg), end = div_i64((wg + 1) * total, nwg);
+        if (pre <= cur && cur < pre + u) {
+          first_work = w;
+          plan[0] = lane;
+          plan[1] = cur - pre;
+          plan[2] = cur;
+          plan[3] = end;
+        }
+      }
     }
   } else {
-    int64_t sum = 0;
-    for (int64_t s0 = 0; s0 < a.b.seqs && sum <= cur; s0 += kFewThreads) {
-      const int64_t s = s0 + tid;
-      u = 0;
-      if (s < a.b.seqs) {
-        const SeqWork w = seq_work(a, s, kRows, tokens_tile);
-        u = w.rtiles * w.ttiles;
+    int64_t total = 0;
+    for (int32_t s0 = 0; s0 < (int32_t)a.b.seqs; s0 += kThreads) {
+      const int32_t s = s0 + tid;
+      int64_t u = 0;
+      if (s < (int32_t)a.b.seqs) {
+        const SeqWork w = seq_work<kRows>(a, s);
+        u = (int64_t)w.rtiles * w.ttiles;
       }
       int64_t chunk;
-      pre = sum + few_scan(u, &chunk);
+      const int64_t pre = total + few_scan<kWaves>(u, &chunk);
+      total += chunk;
+      if (blockIdx.x == 0 && s < (int32_t)a.b.seqs) a.prefix[s] = pre;
+    }
+    if (blockIdx.x == 0 && tid == 0) a.prefix[a.b.seqs] = total;
+    const int nwg = sharing(a, total);
+    if (wg >= nwg) return;
+    const int64_t cur = div_i64(wg * total, nwg), end = div_i64((wg + 1) * total, nwg);
+    int64_t sum = 0;
+    for (int32_t s0 = 0; s0 < (int32_t)a.b.seqs && sum <= cur; s0 += kThreads) {
+      const int32_t s = s0 + tid;
+      int64_t u = 0;
+      SeqWork w;
+      if (s < (int32_t)a.b.seqs) {
+        w = seq_work<kRows>(a, s);
+        u = (int64_t)w.rtiles * w.ttiles;
+      }
+      int64_t chunk;
+      const int64_t pre = sum + few_scan<kWaves>(u, &chunk);
       sum += chunk;
       if (pre <= cur && cur < pre + u) {
-        start[0] = s;
-        start[1] = cur - pre;
+        first_work = w;
+        plan[0] = s;
+        plan[1] = cur - pre;
+        plan[2] = cur;
+        plan[3] = end;
       }
     }
   }
   __syncthreads();
-  int64_t seq = start[0], off = start[1];
+  int32_t seq = __builtin_amdgcn_readfirstlane((int32_t)plan[0]);
+  int64_t off = plan[1], cur = plan[2];
+  const int64_t end = plan[3];
 
-  const float ts_k = MX ? 1.0f : *a.c.tscale[0], ts_v = MX ? 1.0f : *a.c.tscale[1];
-  char* vbuf = lds + wave * L::kBytes;
-  const int64_t head_at = head < (int)a.c.heads ? head : 0;
+  char* vbuf = lds + wave * F::kValues;
+  char* qbuf = lds + kWaves * F::kValues + hh * F::kQ + lane * 16;
+  const uint32_t head_at = head < (int)a.c.heads ? head : 0, heads = (uint32_t)a.c.heads;
+  const uint32_t page_rows = (uint32_t)(a.c.block_size * a.c.heads);
+  const uint32_t pages = a.c.num_blocks < INT32_MAX ? (uint32_t)a.c.num_blocks : (uint32_t)INT32_MAX;
 
+  SeqWork w;
+  {
+    const int32_t* f = reinterpret_cast<const int32_t*>(&first_work);
+    int32_t* t = reinterpret_cast<int32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(SeqWork) / 4); ++i) t[i] = __builtin_amdgcn_readfirstlane(f[i]);
+  }
   while (cur < end) {
-    const SeqWork w = seq_work(a, seq, kRows, tokens_tile);
-    if (w.rtiles == 0) {
-      ++seq;
-      continue;
-    }
-    const int64_t rtile = off / w.ttiles, t0 = off - rtile * w.ttiles;
-    const int64_t n = w.ttiles - t0 < end - cur ? w.ttiles - t0 : end - cur;
-    const int32_t lo = (int32_t)w.lo, hi = (int32_t)w.hi, packed = (int32_t)(w.r.count * a.g);
-    const int32_t* table = a.b.block_table + seq * a.b.max_blocks;
+    const int32_t rtile = off < w.ttiles ? 0 : (int32_t)div_i64(off, w.ttiles), t0 = (int32_t)(off - (int64_t)rtile * w.ttiles);
+    const int32_t n = (int32_t)(w.ttiles - t0 < end - cur ? w.ttiles - t0 : end - cur);
+    const int32_t* table = a.b.block_table + (int64_t)seq * a.b.max_blocks;
 
     // The rows of this tile: row col of sub-tile rt is packed row i g + j, query head head g + j of row i.
-    u32x4v_t q[RT][kTerms][NS];
-    f32x4_t o[RT][2 * NS];
-    float factor[RT], m[RT], l[RT];
-    int32_t pos[RT], first[RT];  // tokens first .. pos are seen
+    u32x4v_t raw[RT][NS];
+    int32_t pos[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int64_t pr = rtile * kRows + 16 * rt + col;
-      const bool live = active && pr < packed;
-      const int32_t i = fastdiv(live ? (int32_t)pr : 0, a.group), j = live ? (int32_t)pr - i * a.g : 0;
-      const int64_t p = w.r.first + i + w.r.shift;
-      pos[rt] = (int32_t)(p < -1 ? -1 : p);
-      first[rt] = a.window > 0 && p - a.window + 1 > 0 ? (int32_t)(p - a.window + 1) : 0;
-      const uint16_t* src = a.q + (w.r.first + i) * a.q_row + (head_at * a.g + j) * a.q_head + quarter * 8 * NS;
-      float amax = 0.0f;
-      u32x4v_t raw[NS];
+      const int32_t pr = rtile * kRows + 16 * rt + col;
+      const bool live = active && pr < w.packed;
+      const int32_t i = live ? fastdiv(pr, a.group) : 0, j = live ? pr - i * a.g : 0;
+      pos[rt] = w.pos + i;
+      const uint16_t* src = a.q + (int64_t)(w.first + i) * a.q_row + (int64_t)(head_at * a.g + j) * a.q_head + quarter * 8 * NS;
 #pragma unroll
-      for (int c = 0; c < NS; ++c) {
-        raw[c] = live ? *reinterpret_cast<const u32x4v_t*>(src + 8 * c) : u32x4v_t{0u, 0u, 0u, 0u};
+      for (int c = 0; c < NS; ++c)
+        raw[rt][c] = live ? *reinterpret_cast<const u32x4v_t*>(src + 8 * c) : u32x4v_t{0u, 0u, 0u, 0u};
+    }
+
+    // A tile of 32 tokens: this wavefront's token col of its half h is token tb + 16 h + col.  First the page ids are
+    // loaded, a tile ahead of the codes, which come a tile ahead of their use.  Tokens behind the last one read its row
+    // (one row for all of them would be a hot line).
+    const int32_t tb0 = w.lo + (t0 * a.tw + slice) * kFewTokens, step = a.tw * kFewTokens;
+    const int32_t last = w.hi > 0 ? w.hi - 1 : 0;
+    int32_t id[2], slot[2];
+    bool inside[2];
+    const auto find = [&](int32_t tile) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(half_to_f32<BF16>(raw[c][e] & 0xFFFFu)), fabsf(half_to_f32<BF16>(raw[c][e] >> 16))));
+      for (int h = 0; h < 2; ++h) {
+        int32_t t = tb0 + tile * step + 16 * h + ltok;
+        const bool in = t < w.hi;
+        t = in ? t : last;
+        const int32_t page = fastdiv(t, a.page);
+        id[h] = table[page];
+        slot[h] = t - page * a.page.d;
+        inside[h] = in;
       }
-      amax = fmaxf(amax, __shfl_xor(amax, 16, 64));
-      amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
+    };
+    uint32_t kc[2][NS], vc[2][NS], ks[2], vs[2];
+    uint32_t row[2], here = 0;  // here: bit 16 h + t, token t of half h is in the cache
+    const auto place = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool paged = (uint32_t)id[h] < pages;
+        row[h] = (paged ? (uint32_t)id[h] : 0u) * page_rows + (uint32_t)slot[h] * heads + head_at;
+        // One lane in four: bits 0, 4, .. of the ballot, closed up.
+        uint64_t bits = __ballot(paged && inside[h]) & 0x1111111111111111ull;
+        bits = (bits | bits >> 3) & 0x0303030303030303ull;
+        bits = (bits | bits >> 6) & 0x000F000F000F000Full;
+        bits = (bits | bits >> 12) & 0x000000FF000000FFull;
+        const uint32_t both = ((uint32_t)bits | (uint32_t)(bits >> 24)) & 0xFFFFu;
+        here = h == 0 ? both : here | both << 16;
+      }
+    };
+    const auto load = [&](int which, int h, uint32_t (&c)[NS], uint32_t& sc) {
+      __builtin_memcpy(c, __builtin_assume_aligned(a.c.codes[which] + (uint64_t)(row[h] * 4 + lquarter) * (4 * NS), kAlign),
+                       4 * NS);
+      if constexpr (SB::kEven) sc = SB::load(a.c.scales[which] + (uint64_t)(row[h] * 4 + lquarter) * SB::kLoad);
+      else sc = SB::load(a.c.scales[which] + (uint64_t)row[h] * SB::kRow + SB::base(lquarter));
+    };
+    if (active) {
+      find(0);
+      place();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load(0, h, kc[h], ks[h]);
+        load(1, h, vc[h], vs[h]);
+      }
+      if (n > 1) find(1);
+    }
+
+    u32x4v_t q[RT][kTerms][F::kQInLds ? 1 : NS];
+    f32x4_t o[RT][2 * NS];
+    float factor[RT], m[RT], l[RT];
+    if (F::kQInLds) __syncthreads();  // the buffers' last use, by other wavefronts
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+      u16x2_t mags = {0, 0};  // magnitude bits order like the values; NaN and infinities on top
+      if constexpr (!MX)
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mags = __builtin_elementwise_max(mags, __builtin_bit_cast(u16x2_t, raw[rt][c][e] & 0x7FFF7FFFu));
+      float amax = 0.0f;
+      if constexpr (!MX) {
+        uint32_t top = mags[0] > mags[1] ? mags[0] : mags[1];
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        amax = half_to_f32<BF16>(top);
+      }
       const RowScale rs = row_scale<MX>(amax, a.scale, ts_k);
       factor[rt] = rs.factor;
 #pragma unroll
-      for (int c = 0; c < NS; ++c)
+      for (int c = 0; c < NS; ++c) {
+        u32x4v_t t[kTerms];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = half_to_f32<BF16>(raw[c][e] & 0xFFFFu) * rs.mul, y = half_to_f32<BF16>(raw[c][e] >> 16) * rs.mul;
-          const uint32_t t = pack2<MX>(x, y);
-          q[rt][0][c][e] = t;
-          if constexpr (kTerms == 2) q[rt][kTerms - 1][c][e] = pack2_rest(x, y, t);
+          const float x = half_to_f32<BF16>(raw[rt][c][e] & 0xFFFFu) * rs.mul, y = half_to_f32<BF16>(raw[rt][c][e] >> 16) * rs.mul;
+          t[0][e] = pack2<MX>(x, y);
+          if constexpr (kTerms == 2) t[kTerms - 1][e] = pack2_rest(x, y, t[0][e]);
         }
+#pragma unroll
+        for (int x = 0; x < kTerms; ++x) {
+          if constexpr (!F::kQInLds) q[rt][x][c] = t[x];
+          else if (slice == 0) *reinterpret_cast<u32x4v_t*>(qbuf + ((rt * kTerms + x) * NS + c) * 1024) = t[x];
+        }
+      }
 #pragma unroll
       for (int d = 0; d < 2 * NS; ++d) o[rt][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       m[rt] = -__builtin_inff();
       l[rt] = 0.0f;
     }
-    // Tokens that every row of the tile sees.
-    const int64_t i0 = rtile * kRows / a.g;
-    const int64_t i1 = ((rtile + 1) * kRows - 1) / a.g < w.r.count ? ((rtile + 1) * kRows - 1) / a.g : w.r.count - 1;
-    const int64_t all_pos = w.r.first + i0 + w.r.shift;
-    const int64_t all_first = a.window > 0 ? w.r.first + i1 + w.r.shift - a.window + 1 : 0;
+    if (F::kQInLds) __syncthreads();
+    // Tokens all_first .. all_pos are seen by every row of the tile.
+    const int32_t in_tile = w.packed - rtile * kRows < kRows ? w.packed - rtile * kRows : kRows;
+    const int32_t all_pos = w.pos + fastdiv(rtile * kRows, a.group);
+    const int32_t last_pos = w.pos + fastdiv(rtile * kRows + in_tile - 1, a.group);
+    const int32_t all_first = a.window > 0 && last_pos >= a.window ? last_pos - a.window + 1 : 0;
 
-    const auto base_of = [&](int64_t tile) { return lo + (int32_t)((t0 + tile) * a.tw + slice) * kFewTokens; };
-    // Cache rows of this lane's two tokens of a tile, -1 where there is none.
-    const auto find = [&](int64_t tile, int64_t (&row)[2]) {
+    // Loads that four neighbouring lanes make of one row reach the cache as one access, in the products' order they would
+    // be four (16 streams of up to 8192 tokens: 28.8 instead of 31.8 us); a key's pieces change lanes afterwards.
+    uint32_t kt[NS], kst;
+    const auto take_k = [&](int h) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        row[h] = -1;
-        const int32_t t = base_of(tile) + 16 * h + col;
-        if (active && tile < n && t < hi) {
-          const int32_t page = fastdiv(t, a.page);
-          const int64_t id = table[page];
-          if (id >= 0 && id < a.c.num_blocks)
-            row[h] = (id * a.c.block_size + (t - page * a.page.d)) * a.c.heads + head_at;
-        }
-      }
+      for (int c = 0; c < NS; ++c) kt[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(turn, (int)kc[h][c]);
+      kst = (uint32_t)__builtin_amdgcn_ds_bpermute(turn, (int)ks[h]);
     };
-    const auto load = [&](const int64_t (&row)[2], FewTile<NS>& t) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        t.there[h] = (uint32_t)__ballot(row[h] >= 0) & 0xFFFFu;
-        const int64_t r = row[h] >= 0 ? row[h] : 0;
-        const uint32_t* kc = reinterpret_cast<const uint32_t*>(a.c.codes[0] + r * (kD / 2)) + quarter * NS;
-        const uint32_t* vc = reinterpret_cast<const uint32_t*>(a.c.codes[1] + r * (kD / 2)) + quarter * NS;
-        __builtin_memcpy(t.k[h], kc, 4 * NS);
-        t.ks[h] = SB::load(a.c.scales[0] + r * SB::kRow + SB::base(quarter));
-        __builtin_memcpy(t.v[h], vc, 4 * NS);
-        t.vs[h] = SB::load(a.c.scales[1] + r * SB::kRow + SB::base(quarter));
-        if (row[h] < 0) {  // values of tokens that are not there count as 0, whatever lies in the cache
-#pragma unroll
-          for (int c = 0; c < NS; ++c) t.v[h][c] = 0;
-          t.vs[h] = 0;
-        }
-      }
-    };
-    const auto compute = [&](int64_t tile, const FewTile<NS>& t) {
-      const int32_t tb = base_of(tile);
-      const bool masked = t.there[0] != 0xFFFFu || t.there[1] != 0xFFFFu || tb + 31 > all_pos || tb < all_first;
+    // One tile; its registers take the next one's codes as soon as they are decoded.
+    const auto compute = [&](int32_t tile) {
+      const int32_t tb = tb0 + tile * step;
+      const uint32_t there = here;
+      const bool masked = there != 0xFFFFFFFFu || tb + 31 > all_pos || tb < all_first;
+      const auto seen = [&](int rt, int t) {
+        return ((there >> t) & 1u) && tb + t <= pos[rt] && (a.window == 0 || tb + t > pos[rt] - a.window);
+      };
+      const bool more = tile + 1 < n;
+      if (more) place();
       f32x4_t sc[RT][2];
+      if constexpr (F::kQInLds) {
+        u32x4v_t kf[2][NS];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4v_t kf[NS];
-        decode_quarter<MX, NS>(t.k[h], t.ks[h], quarter, kf);
+        for (int h = 0; h < 2; ++h) {
+          take_k(h);
+          decode_quarter<MX, NS>(kt, kst, quarter, kf[h]);
+          if (more) load(0, h, kc[h], ks[h]);
+        }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          sc[rt][0] = sc[rt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int x = 0; x < kTerms; ++x)
 #pragma unroll
-            for (int c = 0; c < NS; ++c) acc = mfma16<MX>(kf[c], q[rt][x][c], acc);
-          sc[rt][h] = acc;
+            for (int c = 0; c < NS; ++c) {
+              const u32x4v_t qf = *reinterpret_cast<const u32x4v_t*>(qbuf + ((rt * kTerms + x) * NS + c) * 1024);
+              sc[rt][0] = mfma16<MX>(kf[0][c], qf, sc[rt][0]);
+              sc[rt][1] = mfma16<MX>(kf[1][c], qf, sc[rt][1]);
+            }
         }
-        u32x4v_t vf[NS];
-        decode_quarter<MX, NS>(t.v[h], t.vs[h], quarter, vf);
+      } else {
 #pragma unroll
-        for (int c = 0; c < NS; ++c)
-          *reinterpret_cast<u32x4v_t*>(vbuf + (16 * h + col) * L::kRow + (quarter * NS + c) * 16) = vf[c];
+        for (int h = 0; h < 2; ++h) {
+          u32x4v_t kf[NS];
+          __builtin_amdgcn_sched_barrier(0);
+          take_k(h);
+          decode_quarter<MX, NS>(kt, kst, quarter, kf);
+          if (more) load(0, h, kc[h], ks[h]);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            sc[rt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+              for (int c = 0; c < NS; ++c) sc[rt][h] = mfma16<MX>(kf[c], q[rt][x][c], sc[rt][h]);
+          }
+        }
       }
-      wave_lds_sync();
-      // Some row sees a token that another does not: where its value is not finite, 0 times it is not 0.
-      const bool apart = masked && __any(scale_nonfinite<MX>(t.vs[0], SB::kLoad) || scale_nonfinite<MX>(t.vs[1], SB::kLoad));
-      u32x4v_t pf[RT][kTerms];
-      float pw[RT][2][4];
+      __builtin_amdgcn_sched_barrier(0);
+      i16x4_t pf[RT][kTerms][2];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float top = -__builtin_inff();
@@ -257,14 +369,9 @@ __global__ void __launch_bounds__(kFewThreads) kv_attend_few_kernel(AttendArgs a
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float s = sc[rt][h][e] * factor[rt];
-            if (masked) {
-              const int32_t tok = tb + 16 * h + 4 * quarter + e;
-              const bool seen = (t.there[h] >> (4 * quarter + e)) & 1u && tok <= pos[rt] && tok >= first[rt];
-              s = seen ? s : -__builtin_inff();
-            }
-            sc[rt][h][e] = s;
-            top = fmaxf(top, s);
+            sc[rt][h][e] *= factor[rt];
+            if (masked) sc[rt][h][e] = seen(rt, 16 * h + 4 * quarter + e) ? sc[rt][h][e] : -__builtin_inff();
+            top = fmaxf(top, sc[rt][h][e]);
           }
         if (__any(top > m[rt] + kSlack)) {
           top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -279,71 +386,82 @@ __global__ void __launch_bounds__(kFewThreads) kv_attend_few_kernel(AttendArgs a
         const float mm = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - kWeightBias;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            pw[rt][h][e] = __builtin_amdgcn_exp2f(sc[rt][h][e] - mm);
-            l[rt] += pw[rt][h][e];
+            p[e] = __builtin_amdgcn_exp2f(sc[rt][h][e] - mm);
+            l[rt] += p[e];
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t p = pack2<MX>(pw[rt][h][2 * e], pw[rt][h][2 * e + 1]);
-            pf[rt][0][2 * h + e] = p;
-            if constexpr (kTerms == 2) pf[rt][kTerms - 1][2 * h + e] = pack2_rest(pw[rt][h][2 * e], pw[rt][h][2 * e + 1], p);
-          }
+          const uint32_t x = pack2<MX>(p[0], p[1]), y = pack2<MX>(p[2], p[3]);
+          pf[rt][0][h] = __builtin_bit_cast(i16x4_t, (uint64_t)x | (uint64_t)y << 32);
+          if constexpr (kTerms == 2)
+            pf[rt][kTerms - 1][h] = __builtin_bit_cast(
+                i16x4_t, (uint64_t)pack2_rest(p[0], p[1], x) | (uint64_t)pack2_rest(p[2], p[3], y) << 32);
         }
       }
-      if (!apart) {
-        // Tokens 4 quarter .. + 3 of both half tiles, columns 16 d ..: lane col of a quarter reads row col / 4.
-        const char* at = vbuf + (4 * quarter + (col >> 2)) * L::kRow + (col & 3) * 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t bad = 0;
+        bool any_bad = false;
+        if (masked) {
+          // Values of tokens that are not there count as 0, whatever lies in the cache.
+          const bool gone = !((there >> (16 * h + ltok)) & 1u);
+#pragma unroll
+          for (int c = 0; c < NS; ++c) vc[h][c] = gone ? 0u : vc[h][c];
+          vs[h] = gone ? 0u : vs[h];
+          // A NaN block is taken out (0 times NaN is not 0) and added below to the rows that see it.
+          bad = vs[h];
+          any_bad = false;
+#pragma unroll
+          for (int c = 0; c < NS; ++c) {
+            const bool nan = scale_nonfinite<MX>((bad >> (8 * SB::index(lquarter, c))) & 0xFFu);
+            any_bad = any_bad || nan;
+            vc[h][c] = nan ? 0u : vc[h][c];
+          }
+          any_bad = __any(any_bad);
+          if (any_bad) vs[h] = drop_nan<MX>(vs[h]);
+        }
+        u32x4v_t vf[NS];
+        decode_quarter<MX, NS>(vc[h], vs[h], lquarter, vf);
+        if (more) load(1, h, vc[h], vs[h]);
+        if (h == 1 && tile + 2 < n) find(tile + 2);
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+          *reinterpret_cast<u32x4v_t*>(vbuf + ltok * F::kRow + (lquarter * NS + c) * 16) = vf[c];
+        wave_lds_sync();
+        // Tokens 4 quarter .. + 3, columns 16 d ..: lane col of a quarter reads row col / 4.
+        const char* at = vbuf + (4 * quarter + (col >> 2)) * F::kRow + (col & 3) * 8;
 #pragma unroll
         for (int d = 0; d < 2 * NS; ++d) {
           typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-          const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(__attribute__((address_space(3))) char*)(at + 32 * d));
-          const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(__attribute__((address_space(3))) char*)(at + 32 * d + 16 * L::kRow));
-          const u32x4v_t vt = __builtin_bit_cast(u32x4v_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+          const i16x4_t vt = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_i16x4_t*)(__attribute__((address_space(3))) char*)(at + 32 * d));
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int x2 = 0; x2 < kTerms; ++x2) o[rt][d] = mfma16<MX>(vt, pf[rt][x2], o[rt][d]);
+            for (int x = 0; x < kTerms; ++x) o[rt][d] = mfma16k16<MX>(vt, pf[rt][x][h], o[rt][d]);
         }
-      } else {
-        // Token by token, each row adding only what it sees.
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        if (any_bad) {
 #pragma unroll 1
-          for (int tk = 0; tk < 16; ++tk) {
-            const int32_t tok = tb + 16 * h + tk;
+          for (int t = 0; t < 16; ++t) {
+            uint32_t q4[4];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const float mine = tk & 2 ? (tk & 1 ? pw[rt][h][3] : pw[rt][h][2]) : (tk & 1 ? pw[rt][h][1] : pw[rt][h][0]);
-              const float p = __shfl(mine, (tk >> 2) * 16 + col, 64);
-              const bool seen = (t.there[h] >> tk) & 1u && tok <= pos[rt] && tok >= first[rt];
+            for (int i = 0; i < 4; ++i) q4[i] = (uint32_t)__builtin_amdgcn_readlane((int)bad, 4 * t + i);
 #pragma unroll
-              for (int d = 0; d < 2 * NS; ++d) {
-                const uint16_t* row = reinterpret_cast<const uint16_t*>(vbuf + (16 * h + tk) * L::kRow) + 16 * d + 4 * quarter;
+            for (int d = 0; d < 2 * NS; ++d) {
+              const uint32_t byte = (q4[2 * d / NS] >> (8 * SB::index(2 * d / NS, 2 * d % NS))) & 0xFFu;
+              if (scale_nonfinite<MX>(byte))
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[rt][d][e] += seen ? p * half_to_f32<MX>(row[e]) : 0.0f;
-              }
+                for (int rt = 0; rt < RT; ++rt) o[rt][d] += seen(rt, 16 * h + t) ? __builtin_nanf("") : 0.0f;
             }
           }
+        }
+        wave_lds_sync();
       }
-      wave_lds_sync();
     };
-
-    FewTile<NS> even, odd;
-    int64_t row[2];
-    find(0, row);
-    load(row, even);
-    find(1, row);
-    for (int64_t tile = 0; tile < n; tile += 2) {
-      load(row, odd);
-      find(tile + 2, row);
-      if (active) compute(tile, even);
-      if (tile + 1 >= n) break;
-      load(row, even);
-      find(tile + 3, row);
-      if (active) compute(tile + 1, odd);
-    }
+    if (active)
+      for (int32_t tile = 0; tile < n; ++tile) compute(tile);
 
     // Join the slices; whole sequences' outputs are written, parts kept.
     const bool whole = t0 == 0 && n == w.ttiles;
@@ -352,37 +470,39 @@ __global__ void __launch_bounds__(kFewThreads) kv_attend_few_kernel(AttendArgs a
     for (int rt = 0; rt < RT; ++rt) {
       l[rt] += __shfl_xor(l[rt], 16, 64);
       l[rt] += __shfl_xor(l[rt], 32, 64);
-      __syncthreads();  // the values, or the rows before, are done with
-      float* ob = reinterpret_cast<float*>(vbuf);
-      float2* st = reinterpret_cast<float2*>(vbuf + L::kStats);
+      __syncthreads();  // the values, the queries or the rows before are done with
+      float* ob = reinterpret_cast<float*>(lds + wave * F::kEnd);
 #pragma unroll
       for (int d = 0; d < 2 * NS; ++d)
-        *reinterpret_cast<f32x4_t*>(ob + col * L::kOut + 16 * d + 4 * quarter) = o[rt][d];
-      if (quarter == 0) st[col] = make_float2(m[rt], l[rt]);
+        *reinterpret_cast<f32x4_t*>(ob + col * F::kOut + 16 * d + 4 * quarter) = o[rt][d];
+      if (quarter == 0) reinterpret_cast<float2*>(ob + F::kStats / 4)[col] = make_float2(m[rt], l[rt]);
       __syncthreads();
-      for (int i = tid; i < a.hw * 16 * (kD / 4); i += kFewThreads) {
-        const int d4 = i % (kD / 4), r = i / (kD / 4) % 16, hh = i / (kD / 4) / 16;
-        const int64_t pr = rtile * kRows + 16 * rt + r;
-        if (hg * a.hw + hh >= (int)a.c.heads || pr >= packed) continue;
+      const int live = in_tile - 16 * rt < 16 ? in_tile - 16 * rt : 16;  // rows of this sub-tile
+      const uint32_t per = live > 0 ? 65536u / (uint32_t)live + 1u : 0u;  // hr / live = hr per / 2^16 for hr < 128
+      for (int i = tid; i < a.hw * live * (kD / 4); i += kThreads) {
+        const int d4 = i % (kD / 4), hr = i / (kD / 4), h = (int)((uint32_t)hr * per >> 16), r = hr - h * live;
+        const int32_t pr = rtile * kRows + 16 * rt + r;
+        if (hg * a.hw + h >= (int)a.c.heads) continue;
         float top = -__builtin_inff();
         for (int k = 0; k < a.tw; ++k)
-          top = fmaxf(top, reinterpret_cast<const float2*>(lds + (k * a.hw + hh) * L::kBytes + L::kStats)[r].x);
+          top = fmaxf(top, reinterpret_cast<const float2*>(lds + (k * a.hw + h) * F::kEnd + F::kStats)[r].x);
         const float mm = top == -__builtin_inff() ? 0.0f : top;
         float sum = 0.0f;
         f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < a.tw; ++k) {
-          const char* buf = lds + (k * a.hw + hh) * L::kBytes;
-          const float2 ml = reinterpret_cast<const float2*>(buf + L::kStats)[r];
+          const char* buf = lds + (k * a.hw + h) * F::kEnd;
+          const float2 ml = reinterpret_cast<const float2*>(buf + F::kStats)[r];
           const float f = __builtin_amdgcn_exp2f(ml.x - mm);
           sum += ml.y * f;
-          acc += *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(buf) + r * L::kOut + 4 * d4) * f;
+          acc += *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(buf) + r * F::kOut + 4 * d4) * f;
         }
         if (whole) {
-          const int32_t qi = fastdiv((int32_t)pr, a.group), qj = (int32_t)pr - qi * a.g;
+          const int32_t qi = fastdiv(pr, a.group), qj = pr - qi * a.g;
           const float inv = sum == 0.0f ? 0.0f : ts_v / sum;
-          store_out4<BF16>(a.out + ((w.r.first + qi) * a.q_heads + (hg * a.hw + hh) * a.g + qj) * kD + 4 * d4, acc * inv);
+          store_out4<BF16>(a.out + ((int64_t)(w.first + qi) * a.q_heads + (hg * a.hw + h) * a.g + qj) * kD + 4 * d4,
+                           acc * inv);
         } else {
-          const int at = (hh * RT + rt) * 16 + r;
+          const int at = (h * RT + rt) * 16 + r;
           *reinterpret_cast<f32x4_t*>(part + (int64_t)at * kD + 4 * d4) = acc;
           if (d4 == 0) reinterpret_cast<float2*>(part + (int64_t)a.hw * kRows * kD)[at] = make_float2(top, sum);
         }
@@ -391,91 +511,84 @@ __global__ void __launch_bounds__(kFewThreads) kv_attend_few_kernel(AttendArgs a
     __syncthreads();
     cur += n;
     off += n;
-    if (off == w.rtiles * w.ttiles) {
-      ++seq;
+    if (off == (int64_t)w.rtiles * w.ttiles && cur < end) {
       off = 0;
+      do w = seq_work<kRows>(a, ++seq);
+      while (w.rtiles == 0);
     }
   }
 }
 
 // Joins the parts of one row and query head, if its tokens were shared: their maxima,
-// sums and outputs, in the workgroups' order.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 2048;  // workgroups at most
+// sums and outputs.  A thread loads every part of its 4 elements that it adds at once;
+// the order of the sums depends on the number of parts alone.
+constexpr int kJoinParts = 256;  // workgroups at most
 
-template <bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) kv_attend_join_kernel(AttendArgs a, int rows_tile, int head_dim,
-                                                                      const float* ts_p) {
+template <bool BF16, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_attend_join_kernel(AttendArgs a, int head_dim, const float* ts_p) {
   __shared__ float weight[kJoinParts];
-  __shared__ f32x4_t acc[kJoinThreads];
-  __shared__ float red[kJoinThreads / 64];
-  __shared__ int64_t at[2];
+  __shared__ f32x4_t acc[THREADS];
+  __shared__ float red[2][THREADS / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int64_t r = blockIdx.x;
   const int qh = blockIdx.y;
-  if (tid < 64) {
-    int64_t s = r;
-    if (a.b.row_start) {
-      int64_t lo = 0, hi = a.b.seqs;
-      while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64, x = lo + lane * step;
-        const bool le = x < hi && (int64_t)a.b.row_start[x] <= r;
-        const int n = __popcll(__ballot(le));
-        if (n == 0) break;
-        lo += (int64_t)(n - 1) * step;
-        hi = lo + step < hi ? lo + step : hi;
-      }
-      s = lo;
-    }
-    if (lane == 0) at[0] = s;
-  }
-  __syncthreads();
-  const int64_t s = at[0];
+  int64_t s = r;
+  if (a.b.row_start) s = find_sequence(a.b, r, lane);
   if (s >= a.b.seqs) return;
-  const SeqWork w = seq_work(a, s, rows_tile, kFewTokens * a.tw);
-  if (w.rtiles == 0 || r < w.r.first || r >= w.r.first + w.r.count) return;
-  const int64_t total = a.prefix[a.b.seqs], nwg = sharing(a, total);
+  const int64_t total = a.prefix[a.b.seqs], first = a.prefix[s];
+  const SeqWork w = seq_work<ROWS>(a, (int32_t)s);
   const int head = qh / a.g, hg = head / a.hw, hh = head - hg * a.hw;
-  const int64_t pr = (r - w.r.first) * a.g + (qh - head * a.g), rtile = pr / rows_tile;
-  const int64_t u0 = a.prefix[s] + rtile * w.ttiles, u1 = u0 + w.ttiles;
-  const int64_t w0 = ((u0 + 1) * nwg - 1) / total, w1 = (u1 * nwg - 1) / total;
-  const int parts = (int)(w1 - w0 + 1);
+  const int64_t pr = (r - w.first) * a.g + (qh - head * a.g);
+  if (pr < 0 || pr >= w.packed) return;
+  const int32_t nwg = sharing(a, total), rtile = (int32_t)pr / ROWS;
+  const int64_t u0 = first + (int64_t)rtile * w.ttiles, u1 = u0 + w.ttiles;
+  const int32_t w0 = (int32_t)div_i64((u0 + 1) * nwg - 1, total), w1 = (int32_t)div_i64(u1 * nwg - 1, total);
+  const int parts = w1 - w0 + 1;
   if (parts <= 1) return;
-  const int64_t slot = (int64_t)a.hw * rows_tile * (head_dim + 2);
-  const int64_t row = (int64_t)hh * rows_tile + (pr - rtile * rows_tile);
-  const auto part_of = [&](int p) { return a.part + (((w0 + p) * a.hgroups + hg) * 2 + (p == 0 ? 1 : 0)) * slot; };
-  const auto stats_of = [&](int p) { return reinterpret_cast<const float2*>(part_of(p) + (int64_t)a.hw * rows_tile * head_dim)[row]; };
-  float top = -__builtin_inff();
-  for (int p = tid; p < parts; p += kJoinThreads) {
-    const float m = stats_of(p).x;
-    weight[p] = m;
-    top = fmaxf(top, m);
+  const int64_t slot = (int64_t)a.hw * ROWS * (head_dim + 2);
+  const int64_t row = hh * ROWS + (pr - rtile * ROWS);
+  const auto part_of = [&](int p) { return a.part + (((int64_t)(w0 + p) * a.hgroups + hg) * 2 + (p == 0 ? 1 : 0)) * slot; };
+  float2 st = make_float2(-__builtin_inff(), 0.0f);
+  if (tid < parts) st = reinterpret_cast<const float2*>(part_of(tid) + (int64_t)a.hw * ROWS * head_dim)[row];
+  // The outputs' first loads do not wait for the statistics.
+  constexpr int kAhead = 8;
+  const int quads = head_dim / 4, groups = THREADS / quads, d4 = tid % quads, gi = tid / quads;
+  const auto value_of = [&](int p) { return *reinterpret_cast<const f32x4_t*>(part_of(p) + row * head_dim + 4 * d4); };
+  f32x4_t got[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int p = gi + i * groups;
+    got[i] = gi < groups && p < parts ? value_of(p) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  float top = st.x;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  if (lane == 0) red[tid >> 6] = top;
+  if (lane == 0) red[0][tid >> 6] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  top = red[0][0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 64; ++i) top = fmaxf(top, red[0][i]);
   const float mm = top == -__builtin_inff() ? 0.0f : top;
-  float sum = 0.0f;
-  for (int p = tid; p < parts; p += kJoinThreads) {
-    const float f = __builtin_amdgcn_exp2f(weight[p] - mm);
-    weight[p] = f;
-    sum += f * stats_of(p).y;
-  }
-  sum = wave_sum(sum);
+  const float f = __builtin_amdgcn_exp2f(st.x - mm);
+  if (tid < parts) weight[tid] = f;
+  const float sum_mine = wave_sum(f * st.y);
+  if (lane == 0) red[1][tid >> 6] = sum_mine;
   __syncthreads();
-  if (lane == 0) red[tid >> 6] = sum;
-  __syncthreads();
-  sum = red[0] + red[1] + red[2] + red[3];
-  const int quads = head_dim / 4, groups = kJoinThreads / quads, d4 = tid % quads, gi = tid / quads;
   f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (gi < groups)
-    for (int p = gi; p < parts; p += groups)
-      x += *reinterpret_cast<const f32x4_t*>(part_of(p) + row * head_dim + 4 * d4) * weight[p];
+  if (gi < groups) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int p = gi + i * groups;
+      if (p < parts) x += got[i] * weight[p];
+    }
+    for (int p = gi + kAhead * groups; p < parts; p += groups) x += value_of(p) * weight[p];
+  }
   acc[tid] = x;
   __syncthreads();
   if (gi == 0) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) sum += red[1][i];
     for (int i = 1; i < groups; ++i) x += acc[i * quads + d4];
     const float ts = ts_p ? *ts_p : 1.0f;
     store_out4<BF16>(a.out + (r * a.q_heads + qh) * head_dim + 4 * d4, x * (sum == 0.0f ? 0.0f : ts / sum));
@@ -486,8 +599,10 @@ template <int RT>
 void launch_few(AttendArgs a, bool bf16, hipStream_t s) {
   const dim3 grid((unsigned)(a.nwg * a.hgroups));
   const auto go = [&](auto mx, auto bf, auto ns) {
-    kv_attend_few_kernel<decltype(mx)::value, decltype(bf)::value, decltype(ns)::value, RT>
-        <<<grid, kFewThreads, 0, s>>>(a);
+    constexpr bool kMx = decltype(mx)::value, kBf = decltype(bf)::value;
+    constexpr int kNs = decltype(ns)::value;
+    constexpr int kThreads = 64 * Few<kNs, RT, AttendTypes<kMx, kBf>::kTerms>::kWaves;
+    if constexpr (RT == 1 || kNs <= 4) kv_attend_few_kernel<kMx, kBf, kNs, RT><<<grid, kThreads, 0, s>>>(a);
   };
   const auto dim = [&](auto mx, auto bf) {
     switch (a.c.head_dim / 32) {
@@ -505,10 +620,22 @@ void launch_few(AttendArgs a, bool bf16, hipStream_t s) {
     if (bf16) dim(std::false_type{}, std::true_type{});
     else dim(std::false_type{}, std::false_type{});
   }
-  const dim3 join((unsigned)a.b.rows, (unsigned)a.q_heads);
   const float* ts = a.c.mx ? nullptr : a.c.tscale[1];
-  if (bf16) kv_attend_join_kernel<true><<<join, kJoinThreads, 0, s>>>(a, 16 * RT, (int)a.c.head_dim, ts);
-  else kv_attend_join_kernel<false><<<join, kJoinThreads, 0, s>>>(a, 16 * RT, (int)a.c.head_dim, ts);
+  // 1024 threads take 256 parts of 128 elements at once; with a workgroup a CU and more, 256 threads start sooner (with
+  // 512 in place of either: 16 rows of 40 heads 7.4 instead of 5.6 us, 1 row of 256 parts 9.4 instead of 7.1).
+  const int dim32 = (int)a.c.head_dim;
+  const auto join = [&](auto threads, auto bf) {
+    constexpr int kThreads = decltype(threads)::value;
+    kv_attend_join_kernel<decltype(bf)::value, 16 * RT, kThreads>
+        <<<dim3((unsigned)a.b.rows, (unsigned)a.q_heads), kThreads, 0, s>>>(a, dim32, ts);
+  };
+  if (a.b.rows * a.q_heads < 256) {
+    if (bf16) join(std::integral_constant<int, 1024>{}, std::true_type{});
+    else join(std::integral_constant<int, 1024>{}, std::false_type{});
+  } else {
+    if (bf16) join(std::integral_constant<int, 256>{}, std::true_type{});
+    else join(std::integral_constant<int, 256>{}, std::false_type{});
+  }
 }
 
 // Heads of a workgroup, its token slices, workgroups and 16-row tiles.
@@ -518,14 +645,14 @@ struct FewPlan {
 };
 FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs) {
   FewPlan p;
-  const int64_t groups = (heads + kFewWaves - 1) / kFewWaves;
+  p.rt = rows * (q_heads / heads) > 16 * seqs && head_dim <= 128 ? 2 : 1;
+  const bool wide = head_dim <= 128 && p.rt == 1;
+  const int waves = wide ? 12 : 8, most = 4;
+  const int64_t groups = (heads + most - 1) / most;
   p.hw = (int)((heads + groups - 1) / groups);
   p.hgroups = (int)((heads + p.hw - 1) / p.hw);
-  p.tw = kFewWaves / p.hw;
-  const int per_cu = head_dim > 192 ? 1 : 2;
-  p.nwg = 256 * per_cu / p.hgroups;
-  if (p.nwg < 1) p.nwg = 1;
-  p.rt = rows * (q_heads / heads) > 16 * seqs ? 2 : 1;
+  p.tw = waves / p.hw;
+  p.nwg = (256 + p.hgroups - 1) / p.hgroups;
   p.part_floats = (int64_t)p.nwg * p.hgroups * 2 * p.hw * 16 * p.rt * (head_dim + 2);
   return p;
 }
@@ -545,6 +672,7 @@ void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint1
   a.b = b;
   a.page = make_fastdiv(c.block_size);
   a.group = make_fastdiv(q_heads / c.heads);
+  a.unit = make_fastdiv((int64_t)kFewTokens * p.tw);
   a.cap = b.max_blocks * c.block_size;
   a.q = q;
   a.q_row = q_row;

@@ -43,22 +43,32 @@ struct RopeArgs {
   int interleaved;
 };
 
-// n / d for 0 <= n < 2^31 by one 64-bit product: m = ceil(2^s / d) with s = 31 +
-// ceil(log2 d) overshoots 2^s / d by less than 1, so n m / 2^s overshoots n / d by
-// less than n / 2^s <= 1 / d, which does not reach the next integer.
+// n / d for 0 <= n < 2^31 by the high half of one product: m = ceil(2^(31 + lg) / d)
+// with lg = ceil(log2 d) fits 32 bits and overshoots 2^(31 + lg) / d by less than 1, so
+// n m / 2^(31 + lg) overshoots n / d by less than n / 2^(31 + lg) <= 1 / d, which does not
+// reach the next integer.
 struct FastDiv {
-  uint64_t m;
-  uint32_t s;
+  uint32_t m, lg;
   int32_t d;
 };
 inline FastDiv make_fastdiv(int64_t d) {
   uint32_t lg = 0;
   while (((int64_t)1 << lg) < d) ++lg;
-  const uint32_t s = 31 + lg;
-  return {(((uint64_t)1 << s) + (uint64_t)d - 1) / (uint64_t)d, s, (int32_t)d};
+  const uint64_t one = (uint64_t)1 << (31 + lg);
+  return {(uint32_t)((one + (uint64_t)d - 1) / (uint64_t)d), lg, (int32_t)d};
 }
 __device__ __forceinline__ int32_t fastdiv(int32_t n, const FastDiv& f) {
-  return (int32_t)(((uint64_t)(uint32_t)n * f.m) >> f.s);
+  return (int32_t)(__umulhi((uint32_t)n << 1, f.m) >> f.lg);
+}
+
+// a / b for 0 <= a < 2^52, 0 < b < 2^52: the FP64 quotient, put right by its remainder
+// (a 64-bit integer division takes some 150 instructions).
+__device__ __forceinline__ int64_t div_i64(int64_t a, int64_t b) {
+  int64_t q = (int64_t)((double)a / (double)b);
+  const int64_t r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
 }
 
 // Rows of sequence s inside [0, rows), and where its last token ends:
@@ -78,6 +88,21 @@ __device__ __forceinline__ SeqRows seq_rows(const KvBatch& b, int64_t cap, int64
   r.shift = n - e;
   r.len = n < 0 ? 0 : (n > cap ? cap : n);
   return r;
+}
+
+// The last sequence that starts at or before row r (any sequence if none does), by a
+// wavefront: 64 starts at a time; starts do not fall, so those at or before r come first.
+__device__ __forceinline__ int64_t find_sequence(const KvBatch& b, int64_t r, int lane) {
+  int64_t lo = 0, hi = b.seqs;  // sequences lo .. hi - 1 may hold r
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const bool le = at < hi && (int64_t)b.row_start[at] <= r;
+    const int n = __popcll(__ballot(le));
+    if (n == 0) break;
+    lo += (int64_t)(n - 1) * step;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  return lo;
 }
 
 // ---------------------------------------------------------------------------

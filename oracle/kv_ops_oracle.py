@@ -13,7 +13,7 @@ the rounding to 16 bits).
                  |x| / (scale tscale), at most 6; ties to the even code.  MXFP4: R17.  Values that are not finite: NaN
                  scale, codes 0.  A turned key is rounded to float32 first.
   R24 attention  softmax(scale q . k_t) over the tokens t <= p, t > p - window, that are in the cache; a row that sees
-                 nothing gives zeros.
+                 nothing gives zeros.  MXFP4 blocks whose byte is 253 or 254 count as NaN, like 255.
 """
 from __future__ import annotations
 
@@ -149,7 +149,9 @@ def attention(fmt, cache, q, block_table, seq_lens, row_start, scale, window, we
     rows, q_heads, d = q.shape
     y, bound, mine = np.zeros((rows, q_heads, d)), np.zeros((rows, q_heads, d)), np.zeros(rows, dtype=bool)
     u = 2.0 ** -24
-    kv = [values(fmt, cache[n + "_codes"], cache[n + "_scales"], cache[n + "_tscale"]) for n in "kv"]
+    kv = [values(fmt, cache[n + "_codes"],
+                 np.where(cache[n + "_scales"] >= 253, 255, cache[n + "_scales"]) if fmt == MXFP4 else cache[n + "_scales"],
+                 cache[n + "_tscale"]) for n in "kv"]
     for r, (s, p, _, _) in enumerate(places(rows, block_table, seq_lens, row_start, nb, bs)):
         if s < 0:
             continue
