@@ -22,7 +22,7 @@ LIB_NAME = "libnvfp4.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["nvfp4_abi.hip", "quant_kernels.hip", "gemv.hip", "gemm.hip", "skinny.hip", "small_m.hip", "prefill.hip", "grouped.hip", "kv_gather.hip", "mxfp4.hip", "stream.hip",
            "fp8_abi.hip", "fp8_quant.hip", "fp8_linear.hip", "fp8_gemm.hip",
-           "kv_abi.hip", "rope.hip", "kv_append.hip", "kv_attend_few.hip"]
+           "kv_abi.hip", "rope.hip", "kv_append.hip", "kv_attend_few.hip", "kv_attend_many.hip"]
 
 
 def hipcc() -> str:

@@ -59,6 +59,11 @@ struct AttendArgs {
   int64_t* prefix;          // [seqs + 1] units before each sequence
 };
 
+// Many rows a sequence (kv_attend_many.hip): one workgroup a CU.
+constexpr int kManyWorkgroups = 256;
+int64_t kv_attend_many_workspace_bytes(int64_t head_dim, int64_t g, int64_t rows, int64_t seqs);
+void launch_kv_attend_many(const AttendArgs& a, bool bf16, void* workspace, hipStream_t s);
+
 // 16-bit matrix type and splits by format and query type.
 template <bool MX, bool BF16>
 struct AttendTypes {
@@ -163,6 +168,16 @@ __device__ __forceinline__ u32x4v_t decode8_mx(uint32_t w, float s) {
                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+// Of the 32 tokens from t0 on, those that a row at position pos sees by its place.
+__device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t window, int32_t t0) {
+  const uint32_t to = low_bits(pos - t0 + 1);
+  return window > 0 ? to & ~low_bits(pos - window - t0 + 1) : to;
+}
+
 // A lane's quarter of a cache row: NS pieces of 8.
 template <bool MX, int NS>
 __device__ __forceinline__ void decode_quarter(const uint32_t (&w)[NS], uint32_t sw, int quarter, u32x4v_t (&out)[NS]) {
@@ -196,8 +211,9 @@ template <bool MX>
 __device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts) {
   const float c = scale * ts * kLog2e;
   RowScale r;
-  r.factor = fabsf(c);
-  r.mul = c < 0.0f ? -1.0f : 1.0f;
+  // A factor of 0 goes to the query, so that a masked score, -inf, times the factor stays -inf.
+  r.factor = c == 0.0f ? 1.0f : fabsf(c);
+  r.mul = c == 0.0f ? 0.0f : (c < 0.0f ? -1.0f : 1.0f);
   if constexpr (!MX) {
     const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
     if (amax > 0.0f && e < 255u) {

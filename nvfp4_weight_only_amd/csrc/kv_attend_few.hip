@@ -365,12 +365,14 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float top = -__builtin_inff();
+        uint32_t bits = 0;
+        if (masked) bits = (there & seen_bits(pos[rt], a.window, tb)) >> (4 * quarter);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             sc[rt][h][e] *= factor[rt];
-            if (masked) sc[rt][h][e] = seen(rt, 16 * h + 4 * quarter + e) ? sc[rt][h][e] : -__builtin_inff();
+            if (masked) sc[rt][h][e] = bits & (1u << (16 * h + e)) ? sc[rt][h][e] : -__builtin_inff();
             top = fmaxf(top, sc[rt][h][e]);
           }
         if (__any(top > m[rt] + kSlack)) {
@@ -659,20 +661,22 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
 
 }  // namespace
 
+// Many rows or few, by the packed rows of a sequence on average.
+static bool many_rows(int64_t g, int64_t rows, int64_t seqs) { return rows * g > 32 * seqs; }
+
 int64_t kv_attend_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs) {
+  if (many_rows(q_heads / heads, rows, seqs)) return kv_attend_many_workspace_bytes(head_dim, q_heads / heads, rows, seqs);
   const FewPlan p = few_plan(heads, head_dim, q_heads, rows, seqs);
   return p.part_floats * 4 + (seqs + 2) / 2 * 16;
 }
 
 void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint16_t* q, int64_t q_heads, int64_t q_row,
                       int64_t q_head, float scale, int64_t window, uint16_t* out, void* workspace, hipStream_t s) {
-  const FewPlan p = few_plan(c.heads, c.head_dim, q_heads, b.rows, b.seqs);
-  AttendArgs a;
+  AttendArgs a = {};
   a.c = c;
   a.b = b;
   a.page = make_fastdiv(c.block_size);
   a.group = make_fastdiv(q_heads / c.heads);
-  a.unit = make_fastdiv((int64_t)kFewTokens * p.tw);
   a.cap = b.max_blocks * c.block_size;
   a.q = q;
   a.q_row = q_row;
@@ -682,6 +686,9 @@ void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint1
   a.g = (int32_t)(q_heads / c.heads);
   a.scale = scale;
   a.window = (int32_t)window;
+  if (many_rows(a.g, b.rows, b.seqs)) return launch_kv_attend_many(a, bf16, workspace, s);
+  const FewPlan p = few_plan(c.heads, c.head_dim, q_heads, b.rows, b.seqs);
+  a.unit = make_fastdiv((int64_t)kFewTokens * p.tw);
   a.hw = p.hw;
   a.tw = p.tw;
   a.hgroups = p.hgroups;
