@@ -55,6 +55,7 @@ struct AttendArgs {
   int32_t window;  // 0: none
   int32_t hw, tw, hgroups;  // heads and token slices of a workgroup, groups of heads
   int32_t nwg;              // workgroups of a group of heads
+  int32_t least;            // units of a workgroup, where there are few
   float* part;              // partial results
   int64_t* prefix;          // [seqs + 1] units before each sequence
 };
@@ -79,16 +80,6 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4v_t& a, const u32x4v_t& b, 
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
                                                   0, 0);
-}
-
-// The same on 16 x 16 x 16.
-template <bool MX>
-__device__ __forceinline__ f32x4_t mfma16k16(const i16x4_t& a, const i16x4_t& b, const f32x4_t& c) {
-  typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
-  if constexpr (MX) return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4_t, a), __builtin_bit_cast(f16x4_t, b), c, 0, 0,
-                                                 0);
 }
 
 // Two floats as the matrix type.
@@ -251,7 +242,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int32_t s) {
 // Workgroups that share `total` units: workgroup w of n takes units
 // w total / n up to (w + 1) total / n.
 __device__ __forceinline__ int32_t sharing(const AttendArgs& a, int64_t total) {
-  return total < a.nwg ? (int32_t)total : a.nwg;
+  return total < (int64_t)a.nwg * a.least ? ((int32_t)total + a.least - 1) / a.least : a.nwg;
 }
 
 // 4 outputs of a row.

@@ -1,12 +1,12 @@
 // Attention over a paged FP4 cache for few rows a sequence (decoding, a few drafted
 // tokens): bound by reading the cache.
 //
-// Every workgroup takes an equal, consecutive share of all units (a unit: 32 tw tokens
-// of one tile of rows of one sequence, for hw heads), found from the lengths on the
-// device, so that long and short sequences mix without idle CUs and the host needs no
-// length.  A share that covers a unit list's end in the middle leaves partial results,
-// which kv_attend_join_kernel joins.  A wavefront takes one key/value head and every
-// tw-th tile of 32 tokens: the heads of a group share the lines of codes and scales.
+// Every workgroup takes an equal, consecutive share of all units (a unit: 32 tokens of
+// one tile of rows of one sequence, for hw heads), found from the lengths on the device,
+// so that long and short sequences mix without idle CUs and the host needs no length.
+// A share that ends inside a sequence leaves partial results, which
+// kv_attend_join_kernel joins.  A wavefront takes one key/value head and every tw-th unit
+// of the share: the heads of a group share the lines of codes and scales.
 //
 // A tile: the scores as S^T = K Q^T, tokens by rows.  A lane holds a quarter of a token's
 // key as it lies in memory (16 bytes of codes at 128 elements), which is a fragment of K
@@ -32,13 +32,14 @@ constexpr int kFewTokens = 32;
 template <int NS, int RT, int TERMS>
 struct Few {
   static constexpr int kD = 32 * NS, kRows = 16 * RT;
-  static constexpr int kWaves = NS <= 4 && RT == 1 ? 12 : 8;
-  static constexpr int kHeads = 4;  // of a workgroup, at most
+  static constexpr int kWaves = NS == 8 ? 6 : (NS * RT <= 4 ? 12 : 8);
+  static constexpr int kHeads = NS == 8 ? 2 : 4;  // of a workgroup, at most
   static constexpr bool kQInLds = NS * RT * TERMS > 4;       // queries: more than 16 registers
-  // LDS: 16 tokens' values a wavefront, rows 32 bytes longer than the values, so that 8 rows start in different banks;
+  // LDS: 32 tokens' values a wavefront, rows 32 bytes longer than the values, so that 8 rows start in different banks, and of
+  // tokens 8-15 every two 16-byte pieces change places, so that a write's 16 rows use all of them;
   // the queries; at the end instead a wavefront's 16 rows of outputs with their maximum and sum.
   static constexpr int kRow = 2 * kD + 32;
-  static constexpr int kValues = 16 * kRow;
+  static constexpr int kValues = kFewTokens * kRow;
   static constexpr int kQ = kQInLds ? RT * TERMS * NS * 1024 : 0;
   static constexpr int kOut = kD + 4;  // floats of an output row
   static constexpr int kStats = 16 * kOut * 4;
@@ -204,36 +205,37 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
     // A tile of 32 tokens: this wavefront's token col of its half h is token tb + 16 h + col.  First the page ids are
     // loaded, a tile ahead of the codes, which come a tile ahead of their use.  Tokens behind the last one read its row
     // (one row for all of them would be a hot line).
-    const int32_t tb0 = w.lo + (t0 * a.tw + slice) * kFewTokens, step = a.tw * kFewTokens;
+    const int32_t tb0 = w.lo + (t0 + slice) * kFewTokens, step = a.tw * kFewTokens;
+    const int32_t mine = slice < n && active ? (n - slice + a.tw - 1) / a.tw : 0;  // this slice's tiles: every tw-th
     const int32_t last = w.hi > 0 ? w.hi - 1 : 0;
+    uint32_t kc[2][NS], vc[2][NS], ks[2], vs[2];
+    uint32_t here = 0;  // bit 16 h + t: token t of half h is in the cache
     int32_t id[2], slot[2];
     bool inside[2];
+    uint32_t row[2];
     const auto find = [&](int32_t tile) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         int32_t t = tb0 + tile * step + 16 * h + ltok;
-        const bool in = t < w.hi;
-        t = in ? t : last;
+        inside[h] = t < w.hi;
+        t = inside[h] ? t : last;
         const int32_t page = fastdiv(t, a.page);
         id[h] = table[page];
         slot[h] = t - page * a.page.d;
-        inside[h] = in;
       }
     };
-    uint32_t kc[2][NS], vc[2][NS], ks[2], vs[2];
-    uint32_t row[2], here = 0;  // here: bit 16 h + t, token t of half h is in the cache
     const auto place = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool paged = (uint32_t)id[h] < pages;
         row[h] = (paged ? (uint32_t)id[h] : 0u) * page_rows + (uint32_t)slot[h] * heads + head_at;
         // One lane in four: bits 0, 4, .. of the ballot, closed up.
-        uint64_t bits = __ballot(paged && inside[h]) & 0x1111111111111111ull;
-        bits = (bits | bits >> 3) & 0x0303030303030303ull;
-        bits = (bits | bits >> 6) & 0x000F000F000F000Full;
-        bits = (bits | bits >> 12) & 0x000000FF000000FFull;
-        const uint32_t both = ((uint32_t)bits | (uint32_t)(bits >> 24)) & 0xFFFFu;
-        here = h == 0 ? both : here | both << 16;
+        uint64_t x = __ballot(paged && inside[h]) & 0x1111111111111111ull;
+        x = (x | x >> 3) & 0x0303030303030303ull;
+        x = (x | x >> 6) & 0x000F000F000F000Full;
+        x = (x | x >> 12) & 0x000000FF000000FFull;
+        const uint32_t bits = ((uint32_t)x | (uint32_t)(x >> 24)) & 0xFFFFu;
+        here = h == 0 ? bits : here | bits << 16;
       }
     };
     const auto load = [&](int which, int h, uint32_t (&c)[NS], uint32_t& sc) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
       if constexpr (SB::kEven) sc = SB::load(a.c.scales[which] + (uint64_t)(row[h] * 4 + lquarter) * SB::kLoad);
       else sc = SB::load(a.c.scales[which] + (uint64_t)row[h] * SB::kRow + SB::base(lquarter));
     };
-    if (active) {
+    if (mine > 0) {
       find(0);
       place();
 #pragma unroll
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
         load(0, h, kc[h], ks[h]);
         load(1, h, vc[h], vs[h]);
       }
-      if (n > 1) find(1);
+      if (mine > 1) find(1);
     }
 
     u32x4v_t q[RT][kTerms][F::kQInLds ? 1 : NS];
@@ -311,7 +313,9 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
       for (int c = 0; c < NS; ++c) kt[c] = (uint32_t)__builtin_amdgcn_ds_bpermute(turn, (int)kc[h][c]);
       kst = (uint32_t)__builtin_amdgcn_ds_bpermute(turn, (int)ks[h]);
     };
-    // One tile; its registers take the next one's codes as soon as they are decoded.
+    // One tile; its registers take the next one's codes as soon as they are decoded.  Fragments are read from LDS kAhead
+    // steps before their products (the order is pinned: the compiler would wait for nearly every read).
+    constexpr int kAhead = 4;
     const auto compute = [&](int32_t tile) {
       const int32_t tb = tb0 + tile * step;
       const uint32_t there = here;
@@ -319,8 +323,40 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
       const auto seen = [&](int rt, int t) {
         return ((there >> t) & 1u) && tb + t <= pos[rt] && (a.window == 0 || tb + t > pos[rt] - a.window);
       };
-      const bool more = tile + 1 < n;
+      const bool more = tile + 1 < mine;
       if (more) place();
+      // Values into LDS first: they wait for nothing, and their latency passes under the scores.
+      uint32_t bad[2] = {0, 0}, taken = 0;  // scale words of halves from which NaN blocks were taken out
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (masked) {
+          // Values of tokens that are not there count as 0, whatever lies in the cache.
+          const bool gone = !((there >> (16 * h + ltok)) & 1u);
+#pragma unroll
+          for (int c = 0; c < NS; ++c) vc[h][c] = gone ? 0u : vc[h][c];
+          vs[h] = gone ? 0u : vs[h];
+          // A NaN block is taken out (0 times NaN is not 0) and added below to the rows that see it.
+          bad[h] = vs[h];
+          bool any_bad = false;
+#pragma unroll
+          for (int c = 0; c < NS; ++c) {
+            const bool nan = scale_nonfinite<MX>((bad[h] >> (8 * SB::index(lquarter, c))) & 0xFFu);
+            any_bad = any_bad || nan;
+            vc[h][c] = nan ? 0u : vc[h][c];
+          }
+          if (__any(any_bad)) {
+            vs[h] = drop_nan<MX>(vs[h]);
+            taken |= 1u << h;
+          }
+        }
+        u32x4v_t vf[NS];
+        decode_quarter<MX, NS>(vc[h], vs[h], lquarter, vf);
+        if (more) load(1, h, vc[h], vs[h]);
+        if (h == 1 && tile + 2 < mine) find(tile + 2);
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+          *reinterpret_cast<u32x4v_t*>(vbuf + (16 * h + ltok) * F::kRow + ((lquarter * NS + c) ^ (ltok >> 3)) * 16) = vf[c];
+      }
       f32x4_t sc[RT][2];
       if constexpr (F::kQInLds) {
         u32x4v_t kf[2][NS];
@@ -330,23 +366,25 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
           decode_quarter<MX, NS>(kt, kst, quarter, kf[h]);
           if (more) load(0, h, kc[h], ks[h]);
         }
+        constexpr int kSteps = RT * kTerms * NS;
+        u32x4v_t qf[kAhead];
+        const auto fetch_q = [&](int i) { qf[i % kAhead] = *reinterpret_cast<const u32x4v_t*>(qbuf + i * 1024); };
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          sc[rt][0] = sc[rt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < kAhead; ++i) fetch_q(i);
 #pragma unroll
-          for (int x = 0; x < kTerms; ++x)
+        for (int rt = 0; rt < RT; ++rt) sc[rt][0] = sc[rt][1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < NS; ++c) {
-              const u32x4v_t qf = *reinterpret_cast<const u32x4v_t*>(qbuf + ((rt * kTerms + x) * NS + c) * 1024);
-              sc[rt][0] = mfma16<MX>(kf[0][c], qf, sc[rt][0]);
-              sc[rt][1] = mfma16<MX>(kf[1][c], qf, sc[rt][1]);
-            }
+        for (int i = 0; i < kSteps; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          const int rt = i / (kTerms * NS);
+          sc[rt][0] = mfma16<MX>(kf[0][i % NS], qf[i % kAhead], sc[rt][0]);
+          sc[rt][1] = mfma16<MX>(kf[1][i % NS], qf[i % kAhead], sc[rt][1]);
+          if (i + kAhead < kSteps) fetch_q(i + kAhead);
         }
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           u32x4v_t kf[NS];
-          __builtin_amdgcn_sched_barrier(0);
           take_k(h);
           decode_quarter<MX, NS>(kt, kst, quarter, kf);
           if (more) load(0, h, kc[h], ks[h]);
@@ -360,8 +398,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
           }
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-      i16x4_t pf[RT][kTerms][2];
+      u32x4v_t pf[RT][kTerms];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float top = -__builtin_inff();
@@ -394,76 +431,67 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
             p[e] = __builtin_amdgcn_exp2f(sc[rt][h][e] - mm);
             l[rt] += p[e];
           }
-          const uint32_t x = pack2<MX>(p[0], p[1]), y = pack2<MX>(p[2], p[3]);
-          pf[rt][0][h] = __builtin_bit_cast(i16x4_t, (uint64_t)x | (uint64_t)y << 32);
-          if constexpr (kTerms == 2)
-            pf[rt][kTerms - 1][h] = __builtin_bit_cast(
-                i16x4_t, (uint64_t)pack2_rest(p[0], p[1], x) | (uint64_t)pack2_rest(p[2], p[3], y) << 32);
+          pf[rt][0][2 * h] = pack2<MX>(p[0], p[1]);
+          pf[rt][0][2 * h + 1] = pack2<MX>(p[2], p[3]);
+          if constexpr (kTerms == 2) {
+            pf[rt][kTerms - 1][2 * h] = pack2_rest(p[0], p[1], pf[rt][0][2 * h]);
+            pf[rt][kTerms - 1][2 * h + 1] = pack2_rest(p[2], p[3], pf[rt][0][2 * h + 1]);
+          }
         }
       }
+      wave_lds_sync();
+      // Tokens 4 quarter .. + 3 of both halves, columns 16 d ..: lane col of a quarter reads row col / 4.
+      const char* at = vbuf + (4 * quarter + (col >> 2)) * F::kRow + ((((col >> 1) & 1) ^ (quarter >> 1)) * 16 + (col & 1) * 8);
+      typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+      typedef __attribute__((address_space(3))) char lds_char;
+      u32x4v_t vt[kAhead];
+      const auto fetch_v = [&](int d) {
+        const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds_char*)(at + 32 * d));
+        const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds_char*)(at + 32 * d + 16 * F::kRow));
+        vt[d % kAhead] = __builtin_bit_cast(u32x4v_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int d = 0; d < kAhead; ++d) fetch_v(d);
+#pragma unroll
+      for (int d = 0; d < 2 * NS; ++d) {
         __builtin_amdgcn_sched_barrier(0);
-        uint32_t bad = 0;
-        bool any_bad = false;
-        if (masked) {
-          // Values of tokens that are not there count as 0, whatever lies in the cache.
-          const bool gone = !((there >> (16 * h + ltok)) & 1u);
 #pragma unroll
-          for (int c = 0; c < NS; ++c) vc[h][c] = gone ? 0u : vc[h][c];
-          vs[h] = gone ? 0u : vs[h];
-          // A NaN block is taken out (0 times NaN is not 0) and added below to the rows that see it.
-          bad = vs[h];
-          any_bad = false;
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int c = 0; c < NS; ++c) {
-            const bool nan = scale_nonfinite<MX>((bad >> (8 * SB::index(lquarter, c))) & 0xFFu);
-            any_bad = any_bad || nan;
-            vc[h][c] = nan ? 0u : vc[h][c];
-          }
-          any_bad = __any(any_bad);
-          if (any_bad) vs[h] = drop_nan<MX>(vs[h]);
-        }
-        u32x4v_t vf[NS];
-        decode_quarter<MX, NS>(vc[h], vs[h], lquarter, vf);
-        if (more) load(1, h, vc[h], vs[h]);
-        if (h == 1 && tile + 2 < n) find(tile + 2);
-#pragma unroll
-        for (int c = 0; c < NS; ++c)
-          *reinterpret_cast<u32x4v_t*>(vbuf + ltok * F::kRow + (lquarter * NS + c) * 16) = vf[c];
-        wave_lds_sync();
-        // Tokens 4 quarter .. + 3, columns 16 d ..: lane col of a quarter reads row col / 4.
-        const char* at = vbuf + (4 * quarter + (col >> 2)) * F::kRow + (col & 3) * 8;
-#pragma unroll
-        for (int d = 0; d < 2 * NS; ++d) {
-          typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-          const i16x4_t vt = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4_t*)(__attribute__((address_space(3))) char*)(at + 32 * d));
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int x = 0; x < kTerms; ++x) o[rt][d] = mfma16k16<MX>(vt, pf[rt][x][h], o[rt][d]);
-        }
-        if (any_bad) {
-#pragma unroll 1
-          for (int t = 0; t < 16; ++t) {
-            uint32_t q4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q4[i] = (uint32_t)__builtin_amdgcn_readlane((int)bad, 4 * t + i);
-#pragma unroll
-            for (int d = 0; d < 2 * NS; ++d) {
-              const uint32_t byte = (q4[2 * d / NS] >> (8 * SB::index(2 * d / NS, 2 * d % NS))) & 0xFFu;
-              if (scale_nonfinite<MX>(byte))
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) o[rt][d] += seen(rt, 16 * h + t) ? __builtin_nanf("") : 0.0f;
-            }
-          }
-        }
-        wave_lds_sync();
+          for (int z = 0; z < kTerms; ++z) o[rt][d] = mfma16<MX>(vt[d % kAhead], pf[rt][z], o[rt][d]);
+        if (d + kAhead < 2 * NS) fetch_v(d + kAhead);
       }
+      if (taken) {
+#pragma unroll 1
+        for (int t = 0; t < kFewTokens; ++t) {
+          if (!(taken & (t < 16 ? 1u : 2u))) continue;
+          uint32_t q4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q4[i] = (uint32_t)__builtin_amdgcn_readlane((int)(t < 16 ? bad[0] : bad[1]), 4 * (t & 15) + i);
+#pragma unroll
+          for (int d = 0; d < 2 * NS; ++d) {
+            const uint32_t byte = (q4[2 * d / NS] >> (8 * SB::index(2 * d / NS, 2 * d % NS))) & 0xFFu;
+            if (scale_nonfinite<MX>(byte))
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) o[rt][d] += seen(rt, t) ? __builtin_nanf("") : 0.0f;
+          }
+        }
+      }
+      wave_lds_sync();
     };
-    if (active)
-      for (int32_t tile = 0; tile < n; ++tile) compute(tile);
+    {
+      // A SIMD's wavefronts take turns in priority: left to themselves the oldest runs ahead, and the last runs alone in
+      // the end.
+      int turn_of = (wave >> 2) % 3;
+      for (int32_t tile = 0; tile < mine; ++tile) {
+        if (turn_of == 0) __builtin_amdgcn_s_setprio(0);
+        else if (turn_of == 1) __builtin_amdgcn_s_setprio(1);
+        else __builtin_amdgcn_s_setprio(2);
+        turn_of = turn_of == 2 ? 0 : turn_of + 1;
+        compute(tile);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    }
 
     // Join the slices; whole sequences' outputs are written, parts kept.
     const bool whole = t0 == 0 && n == w.ttiles;
@@ -648,8 +676,8 @@ struct FewPlan {
 FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs) {
   FewPlan p;
   p.rt = rows * (q_heads / heads) > 16 * seqs && head_dim <= 128 ? 2 : 1;
-  const bool wide = head_dim <= 128 && p.rt == 1;
-  const int waves = wide ? 12 : 8, most = 4;
+  const int ns = (int)(head_dim / 32);
+  const int waves = ns == 8 ? 6 : (ns * p.rt <= 4 ? 12 : 8), most = ns == 8 ? 2 : 4;
   const int64_t groups = (heads + most - 1) / most;
   p.hw = (int)((heads + groups - 1) / groups);
   p.hgroups = (int)((heads + p.hw - 1) / p.hw);
@@ -688,7 +716,8 @@ void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint1
   a.window = (int32_t)window;
   if (many_rows(a.g, b.rows, b.seqs)) return launch_kv_attend_many(a, bf16, workspace, s);
   const FewPlan p = few_plan(c.heads, c.head_dim, q_heads, b.rows, b.seqs);
-  a.unit = make_fastdiv((int64_t)kFewTokens * p.tw);
+  a.unit = make_fastdiv(kFewTokens);
+  a.least = p.tw;
   a.hw = p.hw;
   a.tw = p.tw;
   a.hgroups = p.hgroups;

@@ -673,6 +673,7 @@ void launch_kv_attend_many(const AttendArgs& args, bool bf16, void* workspace, h
   AttendArgs a = args;
   a.nwg = kManyWorkgroups;
   a.unit = make_fastdiv(kManyTokens);
+  a.least = 1;
   switch (a.c.head_dim / 32) {
     case 2: return launch_many<2>(a, bf16, workspace, s);
     case 3: return launch_many<3>(a, bf16, workspace, s);
