@@ -36,11 +36,16 @@ constexpr uint32_t kMxNan = 253;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Weights are 2^(s - m + bias) with m at most kSlack (log2 units) below the running
-// maximum, so up to 2^15, FP16's last power of two: one 2^21 below the largest is still a
-// normal FP16 number, and below that it is off by at most 2^-32 of the largest (without
-// the bias by 2^-25, which 10^5 small weights add up to something seen).  Sums keep the
-// bias; it cancels in the quotient.
-constexpr float kSlack = 8.0f, kWeightBias = 7.0f;
+// maximum.  FP16: bias 7, so up to 2^15, its last power of two: a weight 2^21 below the
+// largest is still a normal number, and below that it is off by at most 2^-32 of the
+// largest (without the bias by 2^-25, which 10^5 small weights add up to something seen).
+// BF16 has FP32's range: bias -8, so up to 1, and sums of large MXFP4 values stay in range
+// as long as the result does.  Sums keep the bias; it cancels in the quotient.
+constexpr float kSlack = 8.0f;
+template <bool MX>
+constexpr float weight_bias() {
+  return MX ? -kSlack : 7.0f;
+}
 
 struct AttendArgs {
   KvCache c;

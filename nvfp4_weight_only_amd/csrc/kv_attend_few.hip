@@ -422,7 +422,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
 #pragma unroll
           for (int d = 0; d < 2 * NS; ++d) o[rt][d] *= shrink;
         }
-        const float mm = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - kWeightBias;
+        const float mm = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - weight_bias<MX>();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float p[4];

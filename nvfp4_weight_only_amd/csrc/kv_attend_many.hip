@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
 #pragma unroll
         for (int d = 0; d < NS; ++d) o[d] *= shrink;
       }
-      const float mm = m == -__builtin_inff() ? 0.0f : m - kWeightBias;
+      const float mm = m == -__builtin_inff() ? 0.0f : m - weight_bias<MX>();
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll

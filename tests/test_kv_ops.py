@@ -425,6 +425,11 @@ def check_attention(got, q, c, fmt, table, lens, start, scale, window, left=None
     g = f64(got)
     h = HALF_STEP[q.dtype]
     nan = np.isnan(y) | np.isnan(bound)
+    if q.dtype == torch.float16:
+        # Half a step above FP16's largest number, 65504 + 16, rounding gives infinity: that is the result there.
+        over = ~nan & (np.abs(y) + np.abs(bound) >= 65520)
+        assert (np.isinf(g) | ~over)[mine].all() and (np.sign(g) == np.sign(y))[over & mine[:, None, None]].all()
+        y, g = np.where(over, 0.0, y), np.where(over, 0.0, g)
     off = np.abs(g - y) - (bound + h * (np.abs(y) + bound) + TINY[q.dtype])
     assert np.array_equal(np.isnan(g[mine]), nan[mine])
     assert not (off[mine] > 0)[~nan[mine]].any(), f"{np.nanmax(off[mine])} over, worst at {np.unravel_index(np.nanargmax(off), off.shape)}"
@@ -456,3 +461,300 @@ def test_kv_attention(nv, case, dt, fmt):
         assert torch.equal(again, nv.kv_attention(q[:rows], *args, window=window or None))
     sharp = nv.kv_attention(q[:rows], *args, i32(start), scale=-1.75, window=window or None)
     check_attention(sharp, q[:rows], c, fmt, table, lens, start, -1.75, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("per", [1, 3, 40])
+def test_kv_attention_hidden_values(nv, fmt, per):
+    """NaN blocks, and infinities in the query, reach the rows that see them and no other: tokens above a row, below its
+    window, behind the length, in pages outside the cache."""
+    rng = np.random.default_rng(300 + per)
+    heads, g, d, bs, window = 2, 4, 64, 16, 50
+    lens, n = [130, 200, 61], [per, per, per]
+    nb, table, lens, start = make_batch(rng, lens, n, bs)
+    c = make_cache(rng, fmt, nb, bs, heads, d)
+    q = rand(rng, (3 * per, heads * g, d), torch.float16)
+    nan = 0x7F if fmt == "nvfp4" else 255
+
+    def poison(name, s, t, h, block):
+        c[name][table[s, t // bs], t % bs, h, block] = nan
+    # Behind every length and in every spare slot.
+    for s in range(3):
+        for t in range(int(lens[s]), -(-int(lens[s]) // bs) * bs):
+            c["v_scales"][table[s, t // bs], t % bs] = nan
+            c["k_scales"][table[s, t // bs], t % bs] = nan
+    poison("v_scales", 0, 129, 0, 1)                       # the last token: only its own row sees it
+    poison("v_scales", 0, 130 - per, 1, 0)                 # the first of the call's tokens
+    poison("v_scales", 1, 200 - per - window + 1, 0, 1)    # the first row's window's first token
+    poison("v_scales", 1, 3, 1, 0)                         # below every window
+    poison("k_scales", 2, 60, 1, 0)
+    if fmt == "mxfp4":
+        c["v_scales"][table[2, 2], 5, 0, 0] = 254          # beyond FP32's range: counts as NaN
+        c["v_scales"][table[2, 2], 6, 1, 1] = 252          # still a number
+        c["v_codes"][table[2, 2], 6, 1] = 0x11
+    table[2, 0] = nb + 5                                   # a page outside the cache
+    cache = device_cache(nv, fmt, c)
+    for w in (window, 0):
+        got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), window=w or None)
+        check_attention(got, q, c, fmt, table, lens, start, d ** -0.5, w)
+        assert np.isnan(f64(got)).any() and np.isfinite(f64(got)).any()
+    q[0, 0, 5], q[1 % (3 * per), 3, 7] = float("inf"), float("nan")
+    got = f64(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), window=window))
+    q[0, 0, 5] = q[1 % (3 * per), 3, 7] = 0.0
+    clean = f64(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), window=window))
+    same = np.ones(got.shape[:2], bool)
+    same[0, 0] = same[1 % (3 * per), 3] = False
+    assert np.array_equal(got[same], clean[same], equal_nan=True)
+    assert np.isnan(got[1 % (3 * per), 3]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_kv_attention_values_and_scales_far_apart(nv, fmt):
+    """Queries near the type's largest and smallest numbers, block scales at both ends of their range, tensor scales of
+    0, tiny and negative: the same formula."""
+    rng = np.random.default_rng(9)
+    heads, g, d, bs = 1, 4, 64, 16
+    nb, table, lens, start = make_batch(rng, [100, 33], [2, 1], bs)
+    for dt in (torch.bfloat16, torch.float16):
+        for size, kt in ((1e4, 2.0 ** -14), (1e-4, 4.0), (2.0 ** -12, 0.0), (1.0, -0.25)):
+            c = make_cache(rng, fmt, nb, bs, heads, d)
+            if fmt == "nvfp4":
+                c["k_scales"] = rng.choice([0x00, 0x01, 0x08, 0x30, 0x50, 0x7E], size=c["k_scales"].shape).astype(np.uint8)
+                c["v_scales"] = rng.choice([0x00, 0x01, 0x30, 0x7E], size=c["v_scales"].shape).astype(np.uint8)
+                c["k_tscale"] = np.float32(kt * 2.0 ** -7)
+            else:
+                c["k_scales"] = rng.choice([90, 110, 126, 127], size=c["k_scales"].shape).astype(np.uint8)
+                c["v_scales"] = rng.choice([0, 60, 127, 200], size=c["v_scales"].shape).astype(np.uint8)
+            cache = device_cache(nv, fmt, c)
+            q = rand(rng, (3, heads * g, d), dt, size)
+            scale = 0.125 / size if fmt == "mxfp4" else 0.125
+            got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale)
+            y = f64(got)
+            if dt == torch.float16 and fmt == "mxfp4":
+                continue                                    # 2^73 is no FP16 number
+            check_attention(got, q, c, fmt, table, lens, start, scale, 0)
+            assert np.isfinite(y).all()
+
+
+@pytest.mark.gpu
+def test_kv_attention_many_sequences(nv):
+    """More sequences than a wavefront and a workgroup have lanes, empty ones and empty lengths among them; rows before
+    the first and behind the last are left."""
+    rng = np.random.default_rng(10)
+    for seqs, most in ((65, 40), (900, 9), (1100, 3)):
+        n = rng.integers(0, 2, size=seqs) * rng.integers(1, 3, size=seqs)
+        lens = np.where(rng.random(seqs) < 0.1, 0, n + rng.integers(0, most, size=seqs))
+        nb, table, lens, start = make_batch(rng, lens.tolist(), n.tolist(), 4)
+        start = (start + 3).astype(np.int32)
+        rows = int(start[-1]) + 2
+        c = make_cache(rng, "nvfp4", nb, 4, 2, 64)
+        cache = device_cache(nv, "nvfp4", c)
+        q = rand(rng, (rows, 4, 64), torch.float16)
+        out = torch.full_like(q, 9.0)
+        nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), out=out)
+        check_attention(out, q, c, "nvfp4", table, lens, start, 0.125, 0, left=9.0)
+        k, v = rand(rng, (rows, 2, 64), torch.float16), rand(rng, (rows, 2, 64), torch.float16)
+        nv.kv_append(k, v, cache, i32(table), i32(lens), i32(start))
+        same_cache(host_cache(cache, c), K.append("nvfp4", c, f64(k), f64(v), table, lens, start))
+    # The same through the kernel for many rows.
+    seqs = 1100
+    n = np.where(rng.random(seqs) < 0.97, 0, rng.integers(1, 700, size=seqs))
+    n[5], n[6] = 3000, 0
+    lens = n + rng.integers(0, 3, size=seqs)
+    nb, table, lens, start = make_batch(rng, lens.tolist(), n.tolist(), 32)
+    c = make_cache(rng, "mxfp4", nb, 32, 1, 64)
+    q = rand(rng, (int(start[-1]), 8, 64), torch.bfloat16)
+    cache = device_cache(nv, "mxfp4", c)
+    got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), window=20)
+    check_attention(got, q, c, "mxfp4", table, lens, start, 0.125, 20)
+
+
+@pytest.mark.gpu
+def test_kv_ops_bad_device_data(nv):
+    """Lengths, starts and pages that make no sense: nothing faults, rows that belong to no sequence stay, and sound
+    sequences beside them are right."""
+    rng = np.random.default_rng(11)
+    nb, bs, heads, d = 40, 16, 2, 64
+    c = make_cache(rng, "nvfp4", nb, bs, heads, d)
+    cache = device_cache(nv, "nvfp4", c)
+    table = rng.integers(-50, 100, size=(6, 8)).astype(np.int32)
+    for rows, g in ((12, 2), (64, 8)):
+        q = rand(rng, (rows, heads * g, d), torch.bfloat16)
+        k = rand(rng, (rows, heads, d), torch.bfloat16)
+        for lens in ([-1, 0, 2 ** 31 - 1, -2 ** 31, 50, 129], [5, 128, 3000, 1, 0, 7]):
+            lens = np.array(lens, np.int64)
+            start = np.sort(rng.integers(-3, rows + 4, size=7)).astype(np.int32)
+            out = torch.full_like(q, 2.0)
+            nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), out=out)
+            check_attention(out, q, c, "nvfp4", table, lens, start, d ** -0.5, 0, left=2.0)
+            for start in ([9, 3, 9, 0, 2 ** 31 - 1, -7, 5], [rows] * 7, [0, rows, 0, rows, 0, rows, 0]):
+                nv.kv_attention(q, cache, i32(table), i32(lens), i32(start))
+                nv.kv_append(k, k, cache, i32(np.full_like(table, -1)), i32(lens), i32(start))
+    same_cache(host_cache(cache, c), c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_kv_ops_beyond_32_bits(nv, fmt):
+    """Pages whose codes lie more than 2^32 bytes from the start, and the cache's last page."""
+    rng = np.random.default_rng(12)
+    bs, heads, d = 64, 8, 128
+    nb = 2 ** 32 // (bs * heads * d // 2) + 40
+    shape = (nb, bs, heads)
+    sc = d // K.GROUP[fmt]
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    t = [torch.empty((*shape, w), dtype=torch.uint8, device="cuda") for w in (d // 2, sc, d // 2, sc)]
+    ts = torch.full((1,), 0.02, device="cuda") if fmt == "nvfp4" else None
+    cache = nv.KVCache(*t, ts, ts, fmt)
+    pages = np.array([nb - 1, 3, nb - 20, nb - 39, 7, nb - 2], np.int32)
+    for n, per in (([6 * 64 - 5], 6 * 64 - 5), ([300], 300)):
+        table = pages[None]
+        rows = n[0]
+        k, v = rand(rng, (rows, heads, d), torch.bfloat16), rand(rng, (rows, heads, d), torch.bfloat16)
+        lens, start = np.array(n, np.int32), np.array([0, rows], np.int32)
+        nv.kv_append(k, v, cache, i32(table), i32(lens), i32(start))
+        small = {"k_codes": t[0], "k_scales": t[1], "v_codes": t[2], "v_scales": t[3]}
+        small = {name: x[torch.from_numpy(pages).long().cuda()].cpu().numpy() for name, x in small.items()}
+        small.update(k_tscale=np.float32(0.02) if ts is not None else None, v_tscale=np.float32(0.02) if ts is not None else None)
+        near = np.arange(6, dtype=np.int32)[None]
+        want = K.append(fmt, small, f64(k), f64(v), near, lens, start)
+        same_cache(small, want)
+        for qrows in (1, 40):
+            q = rand(rng, (qrows, heads * 2, d), torch.bfloat16)
+            st = np.array([0, qrows], np.int32)
+            got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(st))
+            check_attention(got, q, small, fmt, near, lens, st, d ** -0.5, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_kv_ops_in_a_row(nv, fmt):
+    """A prompt in two chunks and then single tokens, as a layer runs them: queries turned, keys and values appended,
+    attention.  Every step against the oracle's cache and formula; the gather sees the same cache."""
+    rng = np.random.default_rng(13)
+    heads, g, d, bs, seqs = 2, 3, 64, 16, 3
+    freqs = K.frequencies("ramp", 32, 1e4, 4.0, 64)
+    rope = nv.Rope(nv.rope_frequencies(32, 1e4, "ramp", 4.0, 64), amplitude=1.125)
+    ts = torch.full((1,), 0.01, device="cuda") if fmt == "nvfp4" else None
+    cache = nv.KVCache.zeros(40, bs, heads, d, fmt, ts, ts)
+    c = {n: getattr(cache, n).cpu().numpy() for n in ("k_codes", "k_scales", "v_codes", "v_scales")}
+    c.update(k_tscale=None if ts is None else np.float32(0.01), v_tscale=None if ts is None else np.float32(0.01))
+    table = rng.permutation(40)[:seqs * 8].reshape(seqs, 8).astype(np.int32)
+    lens = np.zeros(seqs, np.int32)
+    for n in ([60, 7, 33], [20, 30, 1], [1, 1, 1], [1, 1, 1], [2, 0, 3]):
+        lens = lens + np.array(n, np.int32)
+        start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        qkv = rand(rng, (int(start[-1]), heads * (g + 2), d), torch.bfloat16)
+        q, k, v = qkv.split([heads * g, heads, heads], 1)
+        pos = np.concatenate([np.arange(m - j, m) for m, j in zip(lens, n)])
+        turned = nv.rope(q, i32(pos), rope)
+        nv.kv_append(k, v, cache, i32(table), i32(lens), i32(start), rope)
+        got = nv.kv_attention(turned, cache, i32(table), i32(lens), i32(start))
+        c = K.append(fmt, c, f64(k), f64(v), table, lens, start, freqs, 1.125)
+        # nv.rope_frequencies' powers differ from the oracle's in their last bits: a key's FP32 rounding may too.
+        mine = host_cache(cache, c)
+        assert all((mine[x] != c[x]).mean() < 1e-3 for x in ("k_codes", "k_scales"))
+        assert np.array_equal(mine["v_codes"], c["v_codes"]) and np.array_equal(mine["v_scales"], c["v_scales"])
+        check_attention(got, turned, mine, fmt, table, lens, start, d ** -0.5, 0)
+    out = torch.zeros((int(lens.sum()), heads, d), dtype=torch.float16, device="cuda")
+    dst = np.concatenate([[0], np.cumsum(lens)[:-1]])
+    nv.kv_gather(cache.k_codes, cache.k_scales, cache.k_tscale, i32(table), i32(lens), i32(dst), out, fmt=fmt)
+    vals = K.values(fmt, mine["k_codes"], mine["k_scales"], mine["k_tscale"])
+    for s in range(seqs):
+        t = np.arange(lens[s])
+        want = vals[table[s, t // bs], t % bs]
+        assert np.abs(f64(out)[dst[s]:dst[s] + lens[s]] - want).max() <= 2.0 ** -11 * np.abs(want).max()
+
+
+@pytest.mark.gpu
+def test_kv_ops_graph_and_streams(nv):
+    """Captured once and replayed with other lengths and inputs, between eager calls; on another stream than the current
+    one at creation; two calls at once on two streams with their own workspaces."""
+    rng = np.random.default_rng(14)
+    heads, g, d, bs, seqs, rows = 2, 4, 128, 16, 4, 8
+    table = rng.permutation(64)[:seqs * 16].reshape(seqs, 16).astype(np.int32)
+    c = make_cache(rng, "nvfp4", 64, bs, heads, d)
+    freqs = torch.from_numpy(K.frequencies(None, d, 1e4)).cuda()
+    rope = nv.Rope(freqs)
+    q, k, v = (rand(rng, (rows, h, d), torch.bfloat16) for h in (heads * g, heads, heads))
+    lens, start, pos = i32([100, 7, 200, 50]), i32([0, 3, 4, 7, 8]), i32(np.arange(rows))
+    tab = i32(table)
+
+    def step(cache):
+        turned = nv.rope(q, pos, rope)
+        nv.kv_append(k, v, cache, tab, lens, start, rope)
+        return nv.kv_attention(turned, cache, tab, lens, start)
+    eager, captured = device_cache(nv, "nvfp4", c), device_cache(nv, "nvfp4", c)
+    step(captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(captured)
+    for i in range(4):
+        lens.copy_(i32([100 + i, 7 + 3 * i, 200 - i, 50 + 11 * i]))
+        q.copy_(rand(rng, q.shape, q.dtype))
+        k.copy_(rand(rng, k.shape, k.dtype))
+        want = step(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        same_cache(host_cache(captured, c), host_cache(eager, c))
+    side = [torch.cuda.Stream() for _ in range(2)]
+    want = step(eager)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s in side:
+            with torch.cuda.stream(s):
+                got.append(nv.kv_attention(nv.rope(q, pos, rope), eager, tab, lens, start))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in got)
+
+
+@pytest.mark.gpu
+def test_kv_ops_binding_refusals(nv):
+    z = torch.zeros
+    cache = nv.KVCache.zeros(4, 16, 2, 64, "mxfp4")
+    q, kv = z((3, 4, 64), dtype=torch.float16, device="cuda"), z((3, 2, 64), dtype=torch.float16, device="cuda")
+    tab, lens = z((3, 2), dtype=torch.int32, device="cuda"), z(3, dtype=torch.int32, device="cuda")
+    rope = nv.Rope(z(16, dtype=torch.float64, device="cuda"))
+    wide = nv.Rope(z(40, dtype=torch.float64, device="cuda"))
+    bad = [
+        lambda: nv.KVCache.zeros(4, 16, 2, 48, "mxfp4"), lambda: nv.KVCache.zeros(4, 16, 2, 64, "nvfp4"),
+        lambda: nv.KVCache.zeros(4, 16, 2, 64, "int4"),
+        lambda: nv.KVCache(cache.k_codes, cache.k_scales, cache.v_codes[:2], cache.v_scales, fmt="mxfp4"),
+        lambda: nv.KVCache(cache.k_codes, cache.k_codes, cache.v_codes, cache.v_scales, fmt="mxfp4"),
+        lambda: nv.KVCache(cache.k_codes.cpu(), cache.k_scales, cache.v_codes, cache.v_scales, fmt="mxfp4"),
+        lambda: nv.Rope(z(12, dtype=torch.float64, device="cuda")), lambda: nv.Rope(z(16, device="cuda")),
+        lambda: nv.rope_frequencies(20), lambda: nv.rope_frequencies(32, scaling="other"),
+        lambda: nv.rope(q.float(), lens, rope), lambda: nv.rope(q.cpu(), lens, rope), lambda: nv.rope(q[0], lens, rope),
+        lambda: nv.rope(q, lens[:2], rope), lambda: nv.rope(q, lens, wide), lambda: nv.rope(q, lens, rope, out=q.bfloat16()),
+        lambda: nv.rope(q.transpose(1, 2), lens, rope), lambda: nv.rope(q, lens, rope, out=q[:2]),
+        lambda: nv.kv_append(kv, kv.bfloat16(), cache, tab, lens), lambda: nv.kv_append(q, q, cache, tab, lens),
+        lambda: nv.kv_append(kv, kv, cache, tab[:2], lens[:2]), lambda: nv.kv_append(kv, kv, cache, tab, lens[:2]),
+        lambda: nv.kv_append(kv, kv, cache, tab, lens, row_start=lens), lambda: nv.kv_append(kv, kv, cache, tab.long(), lens),
+        lambda: nv.kv_append(kv, kv, cache, tab, lens, positions=lens), lambda: nv.kv_append(kv, kv, cache, tab, lens, rope=wide),
+        lambda: nv.kv_attention(q[:, :3], cache, tab, lens), lambda: nv.kv_attention(q, cache, tab, lens, window=0),
+        lambda: nv.kv_attention(q, cache, tab, lens, out=q[:2]), lambda: nv.kv_attention(q, cache, tab, lens.long()),
+        lambda: nv.kv_attention(q, cache, tab, lens, row_start=lens),
+        lambda: nv.kv_attention(q.transpose(0, 1).contiguous().transpose(0, 1)[..., :32], cache, tab, lens),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, RuntimeError)):
+            f()
+            pytest.fail(f"call {i} was not refused")
+    small = nv.KVCache.zeros(4, 16, 2, 32, "mxfp4")
+    with pytest.raises(ValueError):
+        nv.kv_attention(q[..., :32].contiguous(), small, tab, lens)
+    with pytest.raises(nv.NVFP4Error):
+        nv.kv_attention(q, cache, tab, lens, workspace=z(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(nv.NVFP4Error):
+        nv.rope(z((3, 4, 68), dtype=torch.float16, device="cuda")[..., :64], lens, rope)      # strides not multiples of 8
+    # Nothing to do.
+    assert nv.kv_attention(q[:0], cache, tab[:0], lens[:0]).shape == (0, 4, 64)
+    nv.kv_append(kv[:0], kv[:0], cache, tab, lens, row_start=z(4, dtype=torch.int32, device="cuda"))
+    assert nv.rope(q[:0], lens[:0], rope).shape == (0, 4, 64)
