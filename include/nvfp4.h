@@ -587,8 +587,9 @@ typedef struct nvfp4_rope_spec {
  * Products in FP32, rounded once.  inverse turns by -t (with the same amplitude): it is
  * the gradient of the rotation, and undoes one of amplitude 1.  out may be x with the
  * same strides; otherwise they do not overlap, and out's rows and heads do not overlap
- * each other (NVFP4_ERR_SHAPE).  head_dim a multiple of 8, at most 2048.  rows = 0 is a
- * no-op.  x and out 16-byte aligned, freqs 8-byte, positions 4-byte aligned.
+ * each other (NVFP4_ERR_SHAPE).  head_dim a multiple of 8, at most 2048, and at most 2^23
+ * rows.  rows = 0 is a no-op.  x and out 16-byte aligned, freqs 8-byte, positions 4-byte
+ * aligned.
  *
  * nvfp4_rope_frequencies: freqs[i] (double) for i < rot_dim / 2, f = base^(-2 i / rot_dim),
  * for contexts `factor` (at least 1) times as long as the `original` length:
@@ -655,14 +656,15 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * rounded to 11 significant bits (to 2^-32 of the largest where that is more), with MXFP4 to 8
  * bits for BF16 outputs and 15 for FP16 ones.
  * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
- * rows * q_heads < 2^31, and num_blocks * block_size * heads at most 2^30 (others
+ * rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
  * NVFP4_ERR_UNSUPPORTED).
  * Workspace: nvfp4_kv_attention_workspace_bytes bytes (-1: invalid or unsupported shape; no
  * HIP call), any contents, overlapping no argument, not shared by calls in flight at the same
  * time; NULL is NVFP4_ERR_NULL, fewer bytes NVFP4_ERR_SHAPE.
  *
  * Common errors: as nvfp4_kv_gather; q_heads not a multiple of heads is NVFP4_ERR_SHAPE;
- * max_blocks * block_size above 2^31 - 4097 NVFP4_ERR_UNSUPPORTED; codes, scales, k, v, q,
+ * max_blocks * block_size above 2^31 - 4097, rows above 2^23 and seqs above 2^19
+ * NVFP4_ERR_UNSUPPORTED; codes, scales, k, v, q,
  * out and workspace 16-byte aligned, strides as in nvfp4_rope.  rows = 0 or seqs = 0 is a
  * no-op.
  */

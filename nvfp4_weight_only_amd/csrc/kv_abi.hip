@@ -14,7 +14,10 @@ using namespace nvfp4_abi;
 
 constexpr int64_t kMaxHeadDim = 2048;            // angles of a row that fit LDS
 constexpr int64_t kMaxRow = (int64_t)1 << 24;    // elements of a row of heads
-constexpr int64_t kMaxRows = INT32_MAX;
+// Rows, sequences and rows times heads of a call: the launches' threads stay below 2^32.
+constexpr int64_t kMaxRows = (int64_t)1 << 23;
+constexpr int64_t kMaxSeqs = (int64_t)1 << 19;
+constexpr int64_t kMaxRowHeads = (int64_t)1 << 28;
 constexpr int64_t kMaxTokens = INT32_MAX - 4096;  // tokens of a sequence: a tile's end stays an int32
 
 constexpr int64_t kMaxCacheRows = (int64_t)1 << 30;  // tokens times heads that attention addresses
@@ -106,7 +109,7 @@ nvfp4_status check_batch(const nvfp4::KvCache& c, int64_t rows, const int32_t* b
   if (rows < 0 || seqs < 0 || max_blocks <= 0 || !mul_ok(max_blocks, c.block_size, &cap) ||
       !mul_ok(seqs, max_blocks, &entries) || entries > INT64_MAX / 8 || (!row_start && rows != seqs))
     return NVFP4_ERR_SHAPE;
-  if (rows > kMaxRows || seqs > kMaxRows || cap > kMaxTokens) return NVFP4_ERR_UNSUPPORTED;
+  if (rows > kMaxRows || seqs > kMaxSeqs || cap > kMaxTokens) return NVFP4_ERR_UNSUPPORTED;
   *out = {block_table, max_blocks, seq_lens, row_start, seqs, rows};
   if (rows == 0 || seqs == 0) return NVFP4_OK;
   if (!block_table || !seq_lens) return NVFP4_ERR_NULL;
@@ -206,7 +209,8 @@ static bool attention_head_dim(int64_t d) { return d == 64 || d == 96 || d == 12
 int64_t nvfp4_kv_attention_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
                                            int64_t seqs) {
   if (heads <= 0 || q_heads <= 0 || q_heads % heads != 0 || rows < 0 || seqs < 0 || !attention_head_dim(head_dim) ||
-      heads > kMaxRow / head_dim || q_heads > UINT16_MAX || rows > kMaxRows / q_heads || seqs > kMaxRows)
+      heads > kMaxRow / head_dim || q_heads > UINT16_MAX || rows > kMaxRows || rows > kMaxRowHeads / q_heads ||
+      seqs > kMaxSeqs)
     return -1;
   return rows == 0 || seqs == 0 ? 0 : nvfp4::kv_attend_workspace_bytes(heads, head_dim, q_heads, rows, seqs);
 }
@@ -224,7 +228,7 @@ nvfp4_status nvfp4_kv_attention(const nvfp4_kv_cache* cache, int type, const uin
   nvfp4::KvBatch b;
   if ((st = check_batch(c, rows, block_table, max_blocks, seq_lens, row_start, seqs, &b)) != NVFP4_OK) return st;
   if (q_heads <= 0 || q_heads % c.heads != 0 || window < 0 || workspace_bytes < 0) return NVFP4_ERR_SHAPE;
-  if (!attention_head_dim(c.head_dim) || q_heads > UINT16_MAX || rows > kMaxRows / q_heads ||
+  if (!attention_head_dim(c.head_dim) || q_heads > UINT16_MAX || rows > kMaxRowHeads / q_heads ||
       c.num_blocks * c.block_size * c.heads > kMaxCacheRows)
     return NVFP4_ERR_UNSUPPORTED;
   int64_t qb;

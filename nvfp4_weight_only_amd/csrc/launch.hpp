@@ -182,7 +182,7 @@ void launch_rope_frequencies(int scaling, int64_t rot, double base, double facto
 void launch_kv_append(const KvCache& c, const KvBatch& b, bool bf16, const uint16_t* k, const uint16_t* v,
                       int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head, const RopeArgs& rope,
                       const int32_t* positions, hipStream_t s);
-// head_dim 64, 96, 128, 192 or 256; rows * q_heads < 2^31.
+// head_dim 64, 96, 128, 192 or 256; at most 2^23 rows, 2^19 sequences, 2^28 rows * q_heads.
 int64_t kv_attend_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs);
 void launch_kv_attend(const KvCache& c, const KvBatch& b, bool bf16, const uint16_t* q, int64_t q_heads, int64_t q_row,
                       int64_t q_head, float scale, int64_t window, uint16_t* out, void* workspace, hipStream_t s);
