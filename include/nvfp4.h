@@ -648,13 +648,14 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * [0, num_blocks):
  *   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q . k_t),
  * k_t and v_t = E2M1 * scale (* tscale; an MXFP4 block whose byte is 253 or 254, where 6 *
- * 2^(byte - 127) passes FP32's range, counts as NaN as one of 255 does), scores, maxima and sums in FP32, rounded once.
+ * 2^(byte - 127) passes FP32's range, counts as NaN as one of 255 does), scores, maxima and
+ * sums in FP32, rounded once.
  * A row that sees nothing gives zeros; rows of no sequence are left as they were.  Tokens
  * that a row does not see do not touch it, whatever the cache holds there.  Products run on
  * the matrix cores in 16 bits: codes times their block scales are exact there, the
  * query is (or is off by less than 2^-25 of its row's largest element), the weights w_t are
  * rounded to 11 significant bits (to 2^-32 of the largest where that is more), with MXFP4 to 8
- * bits for BF16 outputs and 15 for FP16 ones.
+ * bits for BF16 outputs and 15 for FP16 ones (those below 2^-118 of the largest may be 0).
  * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
  * rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
  * NVFP4_ERR_UNSUPPORTED).

@@ -4,15 +4,15 @@ ONLY: it shares no code, table or helper with the HIP path.
 Plain numpy in float64.  Formats, tables and decoding are those of nvfp4_oracle and kv_oracle (R14, R15; here without
 the rounding to 16 bits).
 
-  R21 rotation   pairs (i, i + rot / 2), or interleaved (2 i, 2 i + 1), of the first rot elements of a head turned by
+  R25 rotation   pairs (i, i + rot / 2), or interleaved (2 i, 2 i + 1), of the first rot elements of a head turned by
                  t = position * freqs[i]: amplitude * (x1 cos t - x2 sin t, x2 cos t + x1 sin t).
-  R22 placement  rows row_start[s] .. row_start[s + 1] - 1 are the last tokens of sequence s: row r is token
+  R26 placement  rows row_start[s] .. row_start[s + 1] - 1 are the last tokens of sequence s: row r is token
                  seq_lens[s] - (row_start[s + 1] - r), in page block_table[s, t // block_size]; rows of no sequence,
                  tokens below 0 or past the table and pages outside [0, num_blocks) are skipped.
-  R23 encoding   NVFP4 with the cache's tensor scale: E4M3 nearest to amax / (6 tscale), at most 448; E2M1 nearest to
+  R27 encoding   NVFP4 with the cache's tensor scale: E4M3 nearest to amax / (6 tscale), at most 448; E2M1 nearest to
                  |x| / (scale tscale), at most 6; ties to the even code.  MXFP4: R17.  Values that are not finite: NaN
                  scale, codes 0.  A turned key is rounded to float32 first.
-  R24 attention  softmax(scale q . k_t) over the tokens t <= p, t > p - window, that are in the cache; a row that sees
+  R28 attention  softmax(scale q . k_t) over the tokens t <= p, t > p - window, that are in the cache; a row that sees
                  nothing gives zeros.  MXFP4 blocks whose byte is 253 or 254 count as NaN, like 255.
 """
 from __future__ import annotations
@@ -27,7 +27,7 @@ from oracle.nvfp4_oracle import (E2M1_TABLE, E4M3_TABLE, _E2M1_MIDS, _E4M3_MIDS,
 
 
 def rotate(x, positions, freqs, amplitude=1.0, interleaved=False):
-    """R21: x [rows, heads, head_dim] float64."""
+    """R25: x [rows, heads, head_dim] float64."""
     x = np.array(x, dtype=np.float64)
     half = len(freqs)
     angle = np.asarray(positions, dtype=np.float64)[:, None] * np.asarray(freqs, dtype=np.float64)
@@ -63,7 +63,7 @@ def frequencies(scaling, rot, base, factor=1.0, original=0.0, low=1.0, high=32.0
 
 
 def encode(fmt, x, tscale=None):
-    """R23: x [..., D] float64 (float32 values) -> (codes [..., D/2], scales [..., D/G])."""
+    """R27: x [..., D] float64 (float32 values) -> (codes [..., D/2], scales [..., D/G])."""
     g = GROUP[fmt]
     x = np.asarray(x, dtype=np.float64)
     blocks = x.reshape(*x.shape[:-1], -1, g)
@@ -101,7 +101,7 @@ def values(fmt, codes, scales, tscale=None):
 
 
 def places(rows, block_table, seq_lens, row_start, num_blocks, block_size):
-    """R22: for each row (sequence, token, page, slot), page -1 where it is skipped, sequence -1 where it has none."""
+    """R26: for each row (sequence, token, page, slot), page -1 where it is skipped, sequence -1 where it has none."""
     seqs, max_blocks = block_table.shape
     out = [(-1, -1, -1, -1)] * rows
     for s in range(seqs):
@@ -118,7 +118,7 @@ def places(rows, block_table, seq_lens, row_start, num_blocks, block_size):
 
 def append(fmt, cache, k, v, block_table, seq_lens, row_start=None, freqs=None, amplitude=1.0, interleaved=False,
            positions=None):
-    """R22, R23: cache = {"k_codes", "k_scales", "k_tscale", "v_..."} (uint8 arrays) -> the same after the call."""
+    """R26, R27: cache = {"k_codes", "k_scales", "k_tscale", "v_..."} (uint8 arrays) -> the same after the call."""
     cache = {n: (c.copy() if isinstance(c, np.ndarray) else c) for n, c in cache.items()}
     nb, bs = cache["k_codes"].shape[:2]
     at = places(len(k), block_table, seq_lens, row_start, nb, bs)
@@ -135,7 +135,7 @@ def append(fmt, cache, k, v, block_table, seq_lens, row_start=None, freqs=None, 
 
 
 def attention(fmt, cache, q, block_table, seq_lens, row_start, scale, window, weight_step):
-    """R24: (y, bound, mine): float64 outputs, how far a kernel's may be off before the output's rounding, and the rows
+    """R28: (y, bound, mine): float64 outputs, how far a kernel's may be off before the output's rounding, and the rows
     that belong to a sequence.
 
     The bound, with u = 2^-24 (half a step of FP32), A_t = |scale| sum |q_i k_ti|: the products' FP32 sum over D elements
@@ -143,8 +143,9 @@ def attention(fmt, cache, q, block_table, seq_lens, row_start, scale, window, we
     the maximum and its base change by 4 u |s_t|, exp2 by 2^-22; a weight's relative error is e to that, so twice the
     exponent's error, plus its rounding (weight_step); sums over n tokens and the joins n u.  Each moves the output by
     sum w |v| / sum w at most, numerator and denominator alike.  Weights in FP16 that lie more than 2^21 below the largest,
-    whose own is at least 2^7 there, are its subnormals: off by 2^-25 / 2^7 of the largest, 2^-32 sum |v| / sum w.  Weights below FP32's smallest
-    normal number, 2^-126, may be 0."""
+    whose own is at least 2^7 there, are its subnormals: off by 2^-25 / 2^7 of the largest, 2^-32 sum |v| / sum w.  With
+    MXFP4 a row's largest weight is held as 2^-8 to 1 (so that sums of its largest values stay in FP32's range), and what
+    falls below FP32's smallest normal number, 2^-126, may be 0: 2^-126 / 2^-8 of the largest, 2^-118 sum |v| / sum w."""
     nb, bs, heads, half = cache["k_codes"].shape
     rows, q_heads, d = q.shape
     y, bound, mine = np.zeros((rows, q_heads, d)), np.zeros((rows, q_heads, d)), np.zeros(rows, dtype=bool)
@@ -176,5 +177,5 @@ def attention(fmt, cache, q, block_table, seq_lens, row_start, scale, window, we
             far = (d + 4) * u * size + 4 * u * np.abs(sc) + 4 * u * np.abs(top) \
                 + 2.0 ** -25 * qmax * abs(scale) * np.abs(k).sum(-1)
             bound[r] = spread * (4 * far.max(0) + 2 * weight_step + 2.0 ** -21 + 2 * (len(page) + 16) * u)[:, None]
-            bound[r] += (2.0 ** -32 if fmt == NVFP4 else 2.0 ** -126) * np.abs(v).sum(0) / total
+            bound[r] += (2.0 ** -32 if fmt == NVFP4 else 2.0 ** -118) * np.abs(v).sum(0) / total
     return y, bound, mine

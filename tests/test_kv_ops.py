@@ -255,7 +255,7 @@ ROPE_CASES = [(1, 1, 16, 16, False), (3, 5, 64, 64, True), (7, 40, 128, 128, Fal
 @pytest.mark.parametrize("dt", list(TYPES))
 @pytest.mark.parametrize("case", ROPE_CASES, ids=lambda c: "x".join(str(int(v)) for v in c))
 def test_rope(nv, case, dt):
-    """Against R21.  FP32 sine and cosine (u each), times the amplitude (u), two products and their sum (u each): 4 u
+    """Against R25.  FP32 sine and cosine (u each), times the amplitude (u), two products and their sum (u each): 4 u
     amplitude (|x1| + |x2|), then half a step of the type."""
     rows, heads, d, rot, il = case
     dt, rng = TYPES[dt], np.random.default_rng(hash(case) % 2 ** 32)
@@ -325,7 +325,7 @@ APPEND_CASES = [
 @pytest.mark.parametrize("dt", list(TYPES))
 @pytest.mark.parametrize("case", range(len(APPEND_CASES)))
 def test_kv_append(nv, case, dt, fmt):
-    """Bit for bit (R22, R23): the whole cache, also where nothing was written."""
+    """Bit for bit (R26, R27): the whole cache, also where nothing was written."""
     lens, n, bs, heads, d, rot, il = APPEND_CASES[case]
     dt, rng = TYPES[dt], np.random.default_rng(100 + case)
     nb, table, lens, start = make_batch(rng, lens, n, bs)
