@@ -374,6 +374,49 @@ def test_kv_append_borders_and_nonfinite(nv, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("ts", [2.0 ** -7, 255 * 2.0 ** -14, 257 * 2.0 ** -15, 0.0078])
+def test_kv_append_every_value(nv, ts, dt):
+    """Every 16-bit value over seven powers of two, beside tops that choose the block's scale: each tie and its nearest
+    neighbours, for tensor scales of 1, 8, 9 and 24 significant bits."""
+    dt, rng = TYPES[dt], np.random.default_rng(12)
+    bits = torch.arange(*(int(torch.tensor(x, dtype=dt).view(torch.int16)) for x in (2.0 ** -4, 2.0 ** 3)), dtype=torch.int16)
+    x = bits.view(dt)
+    tops = torch.tensor([6.0, 7.0, 8.5, 9.0, 10.5, 11.0], dtype=dt)
+    n = -(-x.numel() // 15) * 15
+    x = torch.cat([x, x[:n - x.numel()]]).reshape(1, -1, 15).expand(len(tops), -1, 15)
+    x = torch.cat([tops[:, None, None].expand(-1, x.shape[1], 1), x], -1).reshape(-1, 16)
+    x = torch.cat([x, x[:-len(x) % 8]])
+    x = x.reshape(-1, 2, 64).clone().cuda()
+    rows = len(x)
+    nb, table, lens, start = make_batch(rng, [rows], [rows], 16)
+    c = make_cache(rng, "nvfp4", nb, 16, 2, 64)
+    c["k_tscale"] = c["v_tscale"] = np.float32(ts)
+    cache = device_cache(nv, "nvfp4", c)
+    nv.kv_append(x, -x, cache, i32(table), i32(lens), i32(start))
+    c = K.append("nvfp4", c, f64(x), f64(-x), table, lens, start)
+    same_cache(host_cache(cache, c), c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads, d", [(1, 32), (2, 64), (8, 128), (40, 128)])
+def test_kv_append_short_sequences(nv, heads, d):
+    """Sequences of no, one and a few rows, many of them within a workgroup's."""
+    rng = np.random.default_rng(13)
+    n = rng.choice([0, 0, 0, 1, 2, 5, 40], size=200)
+    lens = n + rng.integers(0, 30, size=200)
+    nb, table, lens, start = make_batch(rng, list(lens), list(n), 16)
+    rows = int(start[-1])
+    c = make_cache(rng, "mxfp4", nb, 16, heads, d)
+    cache = device_cache(nv, "mxfp4", c)
+    k, v = rand(rng, (rows + 3, heads, d), torch.bfloat16), rand(rng, (rows + 3, heads, d), torch.bfloat16)
+    freqs = K.frequencies(None, 32, 1e4)
+    nv.kv_append(k, v, cache, i32(table), i32(lens), i32(start), nv.Rope(torch.from_numpy(freqs).cuda()))
+    c = K.append("mxfp4", c, f64(k), f64(v), table, lens, start, freqs)
+    same_cache(host_cache(cache, c), c)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_kv_append_skips(nv, fmt):
     """Pages outside the cache, tokens below 0 and past the table, rows of no sequence, negative lengths."""
