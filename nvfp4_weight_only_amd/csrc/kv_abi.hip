@@ -149,12 +149,13 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
   nvfp4::RopeArgs turn;
   nvfp4_status st = check_rope(rope, head_dim, &turn);
   if (st != NVFP4_OK) return st;
-  if (head_dim > kMaxHeadDim || heads > kMaxRow / head_dim || rows > kMaxRows) return NVFP4_ERR_UNSUPPORTED;
+  if (head_dim > kMaxHeadDim || heads > kMaxRow / head_dim) return NVFP4_ERR_UNSUPPORTED;
   int64_t xb, ob;
   if ((st = extent(rows, heads, head_dim, &x_row_stride, &x_head_stride, &xb)) != NVFP4_OK ||
       (st = extent(rows, heads, head_dim, &out_row_stride, &out_head_stride, &ob)) != NVFP4_OK)
     return st;
   if (!apart(rows, heads, head_dim, out_row_stride, out_head_stride)) return NVFP4_ERR_SHAPE;
+  if (rows > kMaxRows) return NVFP4_ERR_UNSUPPORTED;
   if (rows == 0) return NVFP4_OK;
   if (!x || !positions || !out) return NVFP4_ERR_NULL;
   if (!aligned16(x) || !aligned16(out) || !aligned_to(positions, 4) ||

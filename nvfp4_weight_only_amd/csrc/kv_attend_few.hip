@@ -651,15 +651,16 @@ void launch_few(AttendArgs a, bool bf16, hipStream_t s) {
     else dim(std::false_type{}, std::false_type{});
   }
   const float* ts = a.c.mx ? nullptr : a.c.tscale[1];
-  // 1024 threads take 256 parts of 128 elements at once; with a workgroup a CU and more, 256 threads start sooner (with
-  // 512 in place of either: 16 rows of 40 heads 7.4 instead of 5.6 us, 1 row of 256 parts 9.4 instead of 7.1).
+  // 1024 threads take 256 parts of 128 elements at once; with a workgroup a CU and more, or sequences too short for many
+  // parts, 256 threads start sooner (with 512 in place of either: 16 rows of 40 heads 7.4 instead of 5.6 us, 1 row of 256
+  // parts 9.4 instead of 7.1; 1 row of 32 parts 5.2 us with 256 threads, 6.1 with 1024).
   const int dim32 = (int)a.c.head_dim;
   const auto join = [&](auto threads, auto bf) {
     constexpr int kThreads = decltype(threads)::value;
     kv_attend_join_kernel<decltype(bf)::value, 16 * RT, kThreads>
         <<<dim3((unsigned)a.b.rows, (unsigned)a.q_heads), kThreads, 0, s>>>(a, dim32, ts);
   };
-  if (a.b.rows * a.q_heads < 256) {
+  if (a.b.rows * a.q_heads < 256 && a.cap > 64 * kFewTokens) {
     if (bf16) join(std::integral_constant<int, 1024>{}, std::true_type{});
     else join(std::integral_constant<int, 1024>{}, std::false_type{});
   } else {
@@ -689,7 +690,10 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
 
 }  // namespace
 
-// Many rows or few, by the packed rows of a sequence on average.
+// Many rows or few, by the packed rows (rows times query heads of a key/value head) of a sequence on average: with 32 (8
+// sequences of up to 16384 tokens, 4 rows each, 32 heads on 4) 37 us by the kernel for few and 47 by the one for many;
+// with 235 (264 rows of 9 sequences, one a chunk, the others single tokens, 16 heads of 256 on 2) 71 by few, 50 by many;
+// with 4092 (7161 rows of 7 prompts, 16 heads of 64 on 4) 419 by few, 96 by many.
 static bool many_rows(int64_t g, int64_t rows, int64_t seqs) { return rows * g > 32 * seqs; }
 
 int64_t kv_attend_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs) {
