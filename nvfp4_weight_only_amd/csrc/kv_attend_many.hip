@@ -15,6 +15,11 @@
 // rows) that some row sees: kv_attend_plan_kernel lists the tiles of rows with the number
 // of units before each.  Workgroups are numbered so that an XCD's are consecutive: they
 // read the same key/value head's tokens from its L2.
+//
+// Measured: 2048 rows behind 6144 tokens (40 query heads on 8 of 128, 3.0e11 operations)
+// 338 us, 0.9 PFLOP/s (a large library product reaches 1.4), plan 5 and join 18: matrix
+// cores busy 43 % of the clocks, vector instructions 50 %, LDS reads 128 bytes a clock in
+// the phases that multiply.
 #include <type_traits>
 
 #include "kv_attend.hpp"
