@@ -27,7 +27,6 @@ namespace nvfp4 {
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef short i16x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
 // MXFP4 scale bytes from here on count as NaN: 6 * 2^(253 - 127) is beyond FP32.

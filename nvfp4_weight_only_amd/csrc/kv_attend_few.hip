@@ -39,7 +39,9 @@ template <int NS, int RT, int TERMS>
 struct Few {
   static constexpr int kD = 32 * NS, kRows = 16 * RT;
   static constexpr int kWaves = NS == 8 ? 6 : (NS * RT <= 4 ? 12 : 8);
-  static constexpr int kHeads = NS == 8 ? 2 : 4;  // of a workgroup, at most
+  // Heads of a workgroup, at most.  4: lines are shared; with 32 rows 2, for smaller parts (8 x 4 rows of 32 heads on 4,
+  // window 4096: 27.6 us and join 6.5 with 2, 29.6 and 7.4 with 4; 16 rows, 16 streams of up to 8192: 33.6 and 29.3).
+  static constexpr int kHeads = NS == 8 || RT == 2 ? 2 : 4;
   static constexpr bool kQInLds = NS * RT * TERMS > 4;       // queries: more than 16 registers
   // LDS: 32 tokens' values a wavefront, rows 32 bytes longer than the values, so that 8 rows start in different banks, and of
   // tokens 8-15 every two 16-byte pieces change places, so that a write's 16 rows use all of them;
@@ -684,7 +686,7 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
   FewPlan p;
   p.rt = rows * (q_heads / heads) > 16 * seqs && head_dim <= 128 ? 2 : 1;
   const int ns = (int)(head_dim / 32);
-  const int waves = ns == 8 ? 6 : (ns * p.rt <= 4 ? 12 : 8), most = ns == 8 ? 2 : 4;
+  const int waves = ns == 8 ? 6 : (ns * p.rt <= 4 ? 12 : 8), most = ns == 8 || p.rt == 2 ? 2 : 4;
   const int64_t groups = (heads + most - 1) / most;
   p.hw = (int)((heads + groups - 1) / groups);
   p.hgroups = (int)((heads + p.hw - 1) / p.hw);
@@ -697,7 +699,7 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
 }  // namespace
 
 // Many rows or few, by the packed rows (rows times query heads of a key/value head) of a sequence on average: with 32 (8
-// sequences of up to 16384 tokens, 4 rows each, 32 heads on 4) 37 us by the kernel for few and 47 by the one for many;
+// sequences of up to 16384 tokens, 4 rows each, 32 heads on 4) 34 us by the kernel for few and 47 by the one for many;
 // with 235 (264 rows of 9 sequences, one a chunk, the others single tokens, 16 heads of 256 on 2) 71 by few, 50 by many;
 // with 4092 (7161 rows of 7 prompts, 16 heads of 64 on 4) 419 by few, 96 by many.
 static bool many_rows(int64_t g, int64_t rows, int64_t seqs) { return rows * g > 32 * seqs; }
