@@ -654,8 +654,9 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * that a row does not see do not touch it, whatever the cache holds there.  Products run on
  * the matrix cores in 16 bits: codes times their block scales are exact there, the
  * query is (or is off by less than 2^-25 of its row's largest element), the weights w_t are
- * rounded to 11 significant bits (to 2^-32 of the largest where that is more), with MXFP4 to 8
- * bits for BF16 outputs and 15 for FP16 ones (those below 2^-118 of the largest may be 0).
+ * rounded to 22 significant bits with NVFP4 (to 2^-32 of the largest where that is more; to 11
+ * bits for BF16 outputs where a sequence has many rows) and to 16 with MXFP4 (those below
+ * 2^-118 of the largest may be 0).
  * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
  * rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
  * NVFP4_ERR_UNSUPPORTED).

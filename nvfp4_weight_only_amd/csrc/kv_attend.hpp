@@ -12,12 +12,19 @@
 // and lies in [2^-10, 2688], so keys and values are exact in FP16, where a pair of
 // codes takes one conversion and one packed product.  The query's row is divided by the
 // power of two of its largest element, so that any BF16 or FP16 row fits FP16 (what
-// lies 2^14 below the largest loses bits, less than 2^-25 of the largest); weights are
-// rounded to FP16.  MXFP4: E2M1 * 2^(byte - 127) needs BF16's range and is exact there,
-// in one conversion a pair (bytes 253 and 254, whose blocks pass FP32's range, count as
-// NaN).  A BF16 query is exact too, and weights are rounded to
-// BF16, half a step of the output's type; for FP16 queries and outputs the query (exactly)
-// and the weights (to 16 bits) are split into two BF16 terms each.
+// lies 2^14 below the largest loses bits, less than 2^-25 of the largest).  MXFP4: E2M1 *
+// 2^(byte - 127) needs BF16's range and is exact there, in one conversion a pair (bytes
+// 253 and 254, whose blocks pass FP32's range, count as NaN).  A BF16 query is exact too; an
+// FP16 one is split into two BF16 terms.
+//
+// Weights are two terms of the matrix type, 22 bits (FP16) or 16 (BF16), so that their
+// rounding stays far below the output's: with one, the distance from the exact result grew
+// by a quarter to a third for FP16 outputs of NVFP4 and BF16 ones of MXFP4 (9 streams with a
+// chunk of 256 rows: 2.67e-4 instead of 2.07e-4, 2.12e-3 instead of 1.66e-3 of the
+// outputs' norm).  The second term costs 1.2 of 34 us at 16 streams of up to 8192 tokens,
+// where memory bounds, and 100 of 330 at 2048 rows behind 6144 (MXFP4, BF16), where products
+// do; so many rows of NVFP4 with BF16 outputs keep one, 11 bits under an output of 8 (1.669e-3
+// and 1.660e-3).
 #pragma once
 
 #include "kv_common.hpp"
@@ -69,10 +76,11 @@ constexpr int kManyWorkgroups = 256;
 int64_t kv_attend_many_workspace_bytes(int64_t head_dim, int64_t g, int64_t rows, int64_t seqs);
 void launch_kv_attend_many(const AttendArgs& a, bool bf16, void* workspace, hipStream_t s);
 
-// 16-bit matrix type and splits by format and query type.
-template <bool MX, bool BF16>
-struct AttendTypes {
-  static constexpr int kTerms = MX && !BF16 ? 2 : 1;
+// Terms of the matrix type that a query and a weight take, by format and query type; MANY: the kernel for many rows.
+template <bool MX, bool BF16, bool MANY>
+struct AttendTerms {
+  static constexpr int kQuery = MX && !BF16 ? 2 : 1;
+  static constexpr int kWeight = MANY && !MX && BF16 ? 1 : 2;
 };
 
 // D = A B + C on 16 x 16 x 32 (A: 16 tokens or dims; B: 16 rows of queries).
@@ -91,9 +99,12 @@ template <bool MX>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return f32x2_to_half<MX>(a, b);
 }
-// What the first term left out, as the matrix type (BF16).
+// What the first term left out, as the matrix type.
+template <bool MX>
 __device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t first) {
-  return f32x2_to_half<true>(a - bf16_to_f32(first & 0xFFFFu), b - __uint_as_float(first & 0xFFFF0000u));
+  if constexpr (MX) return f32x2_to_half<true>(a - bf16_to_f32(first & 0xFFFFu), b - __uint_as_float(first & 0xFFFF0000u));
+  const f16x2_t f = __builtin_bit_cast(f16x2_t, first);  // one mixed product and sum each
+  return f32x2_to_half<false>(__builtin_fmaf((float)f[0], -1.0f, a), __builtin_fmaf((float)f[1], -1.0f, b));
 }
 
 // Scale bytes that a lane needs of a row whose quarter (NS pieces of 8 elements) it holds, and where they are.

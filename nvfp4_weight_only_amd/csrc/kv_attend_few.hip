@@ -81,9 +81,9 @@ __device__ __forceinline__ int64_t few_scan(int64_t v, int64_t* total) {
 }
 
 template <bool MX, bool BF16, int NS, int RT>
-__global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerms>::kWaves))
+__global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>::kQuery>::kWaves))
     kv_attend_few_kernel(AttendArgs a) {
-  constexpr int kTerms = AttendTypes<MX, BF16>::kTerms;
+  constexpr int kTerms = AttendTerms<MX, BF16, false>::kQuery, kWeightTerms = AttendTerms<MX, BF16, false>::kWeight;
   using F = Few<NS, RT, kTerms>;
   using SB = ScaleBytes<MX, NS>;
   constexpr int kWaves = F::kWaves, kThreads = 64 * kWaves, kD = F::kD, kRows = F::kRows;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
         for (int e = 0; e < 4; ++e) {
           const float x = half_to_f32<BF16>(raw[rt][c][e] & 0xFFFFu) * rs.mul, y = half_to_f32<BF16>(raw[rt][c][e] >> 16) * rs.mul;
           t[0][e] = pack2<MX>(x, y);
-          if constexpr (kTerms == 2) t[kTerms - 1][e] = pack2_rest(x, y, t[0][e]);
+          if constexpr (kTerms == 2) t[kTerms - 1][e] = pack2_rest<MX>(x, y, t[0][e]);
         }
 #pragma unroll
         for (int x = 0; x < kTerms; ++x) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
           }
         }
       }
-      u32x4v_t pf[RT][kTerms];
+      u32x4v_t pf[RT][kWeightTerms];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float top = -__builtin_inff();
@@ -441,10 +441,8 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
           }
           pf[rt][0][2 * h] = pack2<MX>(p[0], p[1]);
           pf[rt][0][2 * h + 1] = pack2<MX>(p[2], p[3]);
-          if constexpr (kTerms == 2) {
-            pf[rt][kTerms - 1][2 * h] = pack2_rest(p[0], p[1], pf[rt][0][2 * h]);
-            pf[rt][kTerms - 1][2 * h + 1] = pack2_rest(p[2], p[3], pf[rt][0][2 * h + 1]);
-          }
+          pf[rt][1][2 * h] = pack2_rest<MX>(p[0], p[1], pf[rt][0][2 * h]);
+          pf[rt][1][2 * h + 1] = pack2_rest<MX>(p[2], p[3], pf[rt][0][2 * h + 1]);
         }
       }
       wave_lds_sync();
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTypes<MX, BF16>::kTerm
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int z = 0; z < kTerms; ++z) o[rt][d] = mfma16<MX>(vt[d % kAhead], pf[rt][z], o[rt][d]);
+          for (int z = 0; z < kWeightTerms; ++z) o[rt][d] = mfma16<MX>(vt[d % kAhead], pf[rt][z], o[rt][d]);
         if (d + kAhead < 2 * NS) fetch_v(d + kAhead);
       }
       if (taken) {
@@ -639,7 +637,7 @@ void launch_few(AttendArgs a, bool bf16, hipStream_t s) {
   const auto go = [&](auto mx, auto bf, auto ns) {
     constexpr bool kMx = decltype(mx)::value, kBf = decltype(bf)::value;
     constexpr int kNs = decltype(ns)::value;
-    constexpr int kThreads = 64 * Few<kNs, RT, AttendTypes<kMx, kBf>::kTerms>::kWaves;
+    constexpr int kThreads = 64 * Few<kNs, RT, AttendTerms<kMx, kBf, false>::kQuery>::kWaves;
     if constexpr (RT == 1 || kNs <= 4) kv_attend_few_kernel<kMx, kBf, kNs, RT><<<grid, kThreads, 0, s>>>(a);
   };
   const auto dim = [&](auto mx, auto bf) {

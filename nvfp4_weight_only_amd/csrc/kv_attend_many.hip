@@ -177,7 +177,7 @@ constexpr int64_t many_part_floats() {
 
 template <bool MX, bool BF16, int NS>
 __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(AttendArgs a, ManyPlan p) {
-  constexpr int kTerms = AttendTypes<MX, BF16>::kTerms;
+  constexpr int kTerms = AttendTerms<MX, BF16, true>::kQuery, kWeightTerms = AttendTerms<MX, BF16, true>::kWeight;
   using M = Many<NS>;
   using SB = ScaleBytes<MX, NS>;
   constexpr int kD = M::kD, kRows = M::kRows, kItems = M::kItems, kSteps = 2 * NS;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
       for (int e = 0; e < 4; ++e) {
         const float x = half_to_f32<BF16>(raw[c][e] & 0xFFFFu) * rs.mul, y = half_to_f32<BF16>(raw[c][e] >> 16) * rs.mul;
         q[0][c][e] = pack2<MX>(x, y);
-        if constexpr (kTerms == 2) q[kTerms - 1][c][e] = pack2_rest(x, y, q[0][c][e]);
+        if constexpr (kTerms == 2) q[kTerms - 1][c][e] = pack2_rest<MX>(x, y, q[0][c][e]);
       }
     f32x16_t o[NS];
 #pragma unroll
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
       return ((th[t >> 5] >> (t & 31)) & 1u) && tb + t <= pos && (a.window == 0 || tb + t > pos - a.window);
     };
     f32x16_t s[2];  // register e of s[t] is token 32 t + 8 (e / 4) + 4 half + e % 4
-    u32x4v_t pf[kTerms][4];
+    u32x4v_t pf[kWeightTerms][4];
     const auto weights = [&](int32_t u) {
       const int b = u & 1;
       const int32_t tb = tb0 + u * kManyTokens;
@@ -409,16 +409,17 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
           l += p0 + p1;
           const uint32_t x = pack2<MX>(p0, p1);
           pf[0][2 * t + e / 8][e / 2 % 4] = x;
-          if constexpr (kTerms == 2) pf[kTerms - 1][2 * t + e / 8][e / 2 % 4] = pack2_rest(p0, p1, x);
+          if constexpr (kWeightTerms == 2) pf[kWeightTerms - 1][2 * t + e / 8][e / 2 % 4] = pack2_rest<MX>(p0, p1, x);
         }
     };
     // Scores of unit u, or outputs of unit v, or both: products whose fragments are read kAhead steps before their use
-    // (the order is pinned, since the compiler would wait for nearly every read).  A value's fragment: lane 16 j + i of a
+    // (the order is pinned, since the compiler would wait for nearly every read; with 128 elements and two terms 6 spill
+    // more: 2048 rows behind 6144, MXFP4 and FP16, 650 us instead of 614).  A value's fragment: lane 16 j + i of a
     // transposing read gets column i of tokens 4 half .. + 3 (and 8 on) of a step, columns 32 d + 16 (j % 2) on, and
     // points at row i / 4, columns 4 (i % 4) of them.
     const auto matrix = [&](auto with_scores, auto with_outputs, int32_t u, int32_t v) {
       constexpr int kFirst = decltype(with_scores)::value ? 0 : 4 * NS;
-      constexpr int kEnd = decltype(with_outputs)::value ? 8 * NS : 4 * NS, kAhead = 6;
+      constexpr int kEnd = decltype(with_outputs)::value ? 8 * NS : 4 * NS, kAhead = NS == 4 && kWeightTerms == 2 ? 4 : 6;
       typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
       typedef __attribute__((address_space(3))) char lds_char;
       const char* kbuf = lds + (u & 1) * M::kBuffer + col * M::kKeyRow + 16 * half;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
       for (int i = kFirst; i < kEnd; ++i) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int x = 0; x < kTerms; ++x) {
+        for (int x = 0; x < (i < 4 * NS ? kTerms : kWeightTerms); ++x) {
           if (i < 4 * NS) s[i & 1] = mfma32<MX>(f[i % kAhead], q[x][i >> 1], s[i & 1]);
           else o[(i - 4 * NS) % NS] = mfma32<MX>(f[i % kAhead], pf[x][(i - 4 * NS) / NS], o[(i - 4 * NS) % NS]);
         }
