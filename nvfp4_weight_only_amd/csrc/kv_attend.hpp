@@ -12,10 +12,10 @@
 // and lies in [2^-10, 2688], so keys and values are exact in FP16, where a pair of
 // codes takes one conversion and one packed product.  The query's row is divided by the
 // power of two of its largest element, so that any BF16 or FP16 row fits FP16 (what
-// lies 2^14 below the largest loses bits, less than 2^-25 of the largest).  MXFP4: E2M1 *
-// 2^(byte - 127) needs BF16's range and is exact there, in one conversion a pair (bytes
-// 253 and 254, whose blocks pass FP32's range, count as NaN).  A BF16 query is exact too; an
-// FP16 one is split into two BF16 terms.
+// lies 2^14 below the largest loses bits, less than 2^-25 of the largest) and the products'
+// range hangs on the keys alone.  MXFP4: E2M1 * 2^(byte - 127) needs BF16's range and is
+// exact there, in one conversion a pair (bytes 253 and 254, whose blocks pass FP32's range,
+// count as NaN).  A BF16 query is exact too; an FP16 one is split into two BF16 terms.
 //
 // Weights are two terms of the matrix type, 22 bits (FP16) or 16 (BF16), so that their
 // rounding stays far below the output's: with one, the distance from the exact result grew
@@ -38,8 +38,6 @@ typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
 // MXFP4 scale bytes from here on count as NaN: 6 * 2^(253 - 127) is beyond FP32.
 constexpr uint32_t kMxNan = 253;
-
-constexpr float kLog2e = 1.44269504088896340736f;
 
 // Weights are 2^(s - m + bias) with m at most kSlack (log2 units) below the running
 // maximum.  FP16: bias 7, so up to 2^15, its last power of two: a weight 2^21 below the
@@ -209,24 +207,30 @@ __device__ __forceinline__ void decode_quarter(const uint32_t (&w)[NS], uint32_t
 }
 
 // A row of queries' scale: s = factor * (the product of the matrix type's values) in
-// units of log2; the query's elements times `mul`.
+// units of log2; the query's elements times `mul`, which brings the largest to 1 .. 2.
+// The factor in FP64, since the product of two scales and the row's power of two can leave
+// FP32's range on the way where the scores do not.
 struct RowScale {
   float factor, mul;
 };
-template <bool MX>
 __device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts) {
-  const float c = scale * ts * kLog2e;
+  const double c = (double)scale * (double)ts * 1.4426950408889634074;  // log2 e
+  double f = fabs(c);
   RowScale r;
+  r.mul = c < 0.0 ? -1.0f : 1.0f;
+  const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
+  if (amax > 0.0f && e < 255u) {
+    const int n = (int)e - 127;  // FP32 subnormals (e = 0) by 2^-127
+    f = __builtin_amdgcn_ldexp(f, n);
+    r.mul = __builtin_amdgcn_ldexpf(r.mul, -n);
+  }
+  // A factor beyond FP32 makes scores of any keys but tiny ones overflow or lie far beyond exp2's range from each other.
+  constexpr double kMax = 3.4028234663852886e38;
+  r.factor = f > kMax && f < __builtin_inf() ? (float)kMax : (float)f;
   // A factor of 0 goes to the query, so that a masked score, -inf, times the factor stays -inf.
-  r.factor = c == 0.0f ? 1.0f : fabsf(c);
-  r.mul = c == 0.0f ? 0.0f : (c < 0.0f ? -1.0f : 1.0f);
-  if constexpr (!MX) {
-    const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
-    if (amax > 0.0f && e < 255u) {
-      const int n = (int)e - 127;  // FP32 subnormals (e = 0) by 2^-127
-      r.factor = __builtin_amdgcn_ldexpf(r.factor, n);
-      r.mul = __builtin_amdgcn_ldexpf(r.mul, -n);
-    }
+  if (r.factor == 0.0f) {
+    r.factor = 1.0f;
+    r.mul = 0.0f;
   }
   return r;
 }

@@ -271,20 +271,15 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
     for (int rt = 0; rt < RT; ++rt) {
       typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
       u16x2_t mags = {0, 0};  // magnitude bits order like the values; NaN and infinities on top
-      if constexpr (!MX)
 #pragma unroll
-        for (int c = 0; c < NS; ++c)
+      for (int c = 0; c < NS; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mags = __builtin_elementwise_max(mags, __builtin_bit_cast(u16x2_t, raw[rt][c][e] & 0x7FFF7FFFu));
-      float amax = 0.0f;
-      if constexpr (!MX) {
-        uint32_t top = mags[0] > mags[1] ? mags[0] : mags[1];
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-        amax = half_to_f32<BF16>(top);
-      }
-      const RowScale rs = row_scale<MX>(amax, a.scale, ts_k);
+        for (int e = 0; e < 4; ++e)
+          mags = __builtin_elementwise_max(mags, __builtin_bit_cast(u16x2_t, raw[rt][c][e] & 0x7FFF7FFFu));
+      uint32_t largest = mags[0] > mags[1] ? mags[0] : mags[1];
+      largest = max(largest, (uint32_t)__shfl_xor((int)largest, 16, 64));
+      largest = max(largest, (uint32_t)__shfl_xor((int)largest, 32, 64));
+      const RowScale rs = row_scale(half_to_f32<BF16>(largest), a.scale, ts_k);
       factor[rt] = rs.factor;
 #pragma unroll
       for (int c = 0; c < NS; ++c) {

@@ -265,20 +265,16 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
     for (int c = 0; c < kSteps; ++c)
       raw[c] = live ? *reinterpret_cast<const u32x4v_t*>(src + 16 * c) : u32x4v_t{0u, 0u, 0u, 0u};
     find(0);
-    float amax = 0.0f;
-    if constexpr (!MX) {
-      typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
-      u16x2_t mags = {0, 0};  // magnitude bits order like the values; NaN and infinities on top
+    typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t mags = {0, 0};  // magnitude bits order like the values; NaN and infinities on top
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
+    for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mags = __builtin_elementwise_max(mags, __builtin_bit_cast(u16x2_t, raw[c][e] & 0x7FFF7FFFu));
-      uint32_t top = mags[0] > mags[1] ? mags[0] : mags[1];
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      amax = half_to_f32<BF16>(top);
-    }
-    const RowScale rs = row_scale<MX>(amax, a.scale, ts_k);
+      for (int e = 0; e < 4; ++e)
+        mags = __builtin_elementwise_max(mags, __builtin_bit_cast(u16x2_t, raw[c][e] & 0x7FFF7FFFu));
+    uint32_t largest = mags[0] > mags[1] ? mags[0] : mags[1];
+    largest = max(largest, (uint32_t)__shfl_xor((int)largest, 32, 64));
+    const RowScale rs = row_scale(half_to_f32<BF16>(largest), a.scale, ts_k);
 #pragma unroll
     for (int c = 0; c < kSteps; ++c)
 #pragma unroll

@@ -48,3 +48,30 @@ def test_weights_have_more_bits_than_the_output(nv, shape, dt, fmt):
     q = rand(rng, (64 * per, g, 64), dt)
     got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=0.02)
     within(got, q, c, fmt, table, lens, start, 0.02, 0, weight)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+@pytest.mark.parametrize("fmt, size, kt, scale", [
+    ("nvfp4", 2.0 ** -130, 2.0 ** -24, 0.125),         # scores of nearly 0: the mean of the values that a row sees
+    ("nvfp4", 2.0 ** -130, 2.0 ** 30, 2.0 ** 100),     # the scales' product above FP32's range, scores of ordinary size
+    ("nvfp4", 2.0 ** 125, 2.0 ** -120, 2.0 ** -5),
+    ("nvfp4", 2.0 ** 100, 2.0 ** -60, -2.0 ** -100),   # the scales' product below FP32's range
+    ("mxfp4", 2.0 ** -128, None, 3e38),                # times log2 e above FP32's range
+    ("mxfp4", 2.0 ** -130, None, 0.125),
+    ("mxfp4", 2.0 ** 125, None, 2.0 ** -125),
+])
+def test_far_queries_and_scales(nv, fmt, size, kt, scale, shape):
+    """Queries near BF16's ends with scales that bring the scores back, where every row has tokens that it does not see."""
+    per, g = shape
+    rng = np.random.default_rng(501)
+    lens = rng.integers(per + 1, 90, size=5).tolist()
+    nb, table, lens, start = make_batch(rng, lens, [per] * 5, 16)
+    c = make_cache(rng, fmt, nb, 16, 2, 64)
+    if kt is not None:
+        c["k_tscale"] = np.float32(kt)
+    cache = device_cache(nv, fmt, c)
+    q = torch.from_numpy(np.clip(rng.normal(0, size, size=(5 * per, 2 * g, 64)), -3e38, 3e38)).to(torch.bfloat16).cuda()
+    for window in (None, 7):
+        got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale, window=window)
+        within(got, q, c, fmt, table, lens, start, scale, window or 0, 2.0 ** -11)
