@@ -650,7 +650,8 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * k_t and v_t = E2M1 * scale (* tscale; an MXFP4 block whose byte is 253 or 254, where 6 *
  * 2^(byte - 127) passes FP32's range, counts as NaN as one of 255 does), scores, maxima and
  * sums in FP32, rounded once.
- * A row that sees nothing gives zeros; rows of no sequence are left as they were.  Tokens
+ * A row that sees nothing gives zeros, and one whose query is not finite NaN if it sees a
+ * token; rows of no sequence are left as they were.  Tokens
  * that a row does not see do not touch it, whatever the cache holds there.  Products run on
  * the matrix cores in 16 bits: codes times their block scales are exact there, the
  * query is (or is off by less than 2^-25 of its row's largest element), the weights w_t are

@@ -224,6 +224,9 @@ __device__ __forceinline__ RowScale row_scale(float amax, float scale, float ts)
     f = __builtin_amdgcn_ldexp(f, n);
     r.mul = __builtin_amdgcn_ldexpf(r.mul, -n);
   }
+  // With an infinity in the query every score is one or NaN, and the softmax NaN, also where all are -inf, which would
+  // count as masked.
+  if (e == 255u) r.mul = __builtin_nanf("");
   // A factor beyond FP32 makes scores of any keys but tiny ones overflow or lie far beyond exp2's range from each other.
   constexpr double kMax = 3.4028234663852886e38;
   r.factor = f > kMax && f < __builtin_inf() ? (float)kMax : (float)f;

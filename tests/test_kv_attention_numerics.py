@@ -75,3 +75,29 @@ def test_far_queries_and_scales(nv, fmt, size, kt, scale, shape):
     for window in (None, 7):
         got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale, window=window)
         within(got, q, c, fmt, table, lens, start, scale, window or 0, 2.0 ** -11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_infinite_queries(nv, shape, dt, fmt):
+    """An infinity in a query makes every score one, with positive keys of one sign: the softmax is NaN for -inf as for
+    inf, unless the row sees nothing.  The other rows are as they are without it."""
+    per, g = shape
+    dt, rng = TYPES[dt], np.random.default_rng(502)
+    lens = [1, 40, 90, 0, 400]
+    nb, table, lens, start = make_batch(rng, lens, [per] * 5, 16)
+    c = make_cache(rng, fmt, nb, 16, 1, 64)
+    c["k_codes"] = rng.integers(1, 8, size=c["k_codes"].shape, dtype=np.uint8) * np.uint8(17)
+    cache = device_cache(nv, fmt, c)
+    q = rand(rng, (5 * per, g, 64), dt)
+    clean = f64(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start)))
+    sees = np.array([int(n) - per + i >= 0 for n in lens for i in range(per)])
+    for value in (float("-inf"), float("inf")):
+        x = q.clone()
+        x[:, 1, 9] = value
+        got = f64(nv.kv_attention(x, cache, i32(table), i32(lens), i32(start)))
+        assert np.isnan(got[sees, 1]).all() and (got[~sees, 1] == 0).all()
+        others = [0, *range(2, g)]
+        assert np.array_equal(got[:, others], clean[:, others])
