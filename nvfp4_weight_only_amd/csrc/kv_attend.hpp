@@ -267,6 +267,13 @@ __device__ __forceinline__ int32_t sharing(const AttendArgs& a, int64_t total) {
   return total < (int64_t)a.nwg * a.least ? ((int32_t)total + a.least - 1) / a.least : a.nwg;
 }
 
+// Outputs from sums over tokens and the weights' sum (0: the row sees nothing).  The tensor scale last: its quotient by
+// the sum would lose bits below FP32's range where the outputs do not.
+__device__ __forceinline__ f32x4_t finish(const f32x4_t& v, float sum, float ts) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  return v * inv * (sum == 0.0f ? 0.0f : ts);
+}
+
 // 4 outputs of a row.
 template <bool BF16>
 __device__ __forceinline__ void store_out4(uint16_t* p, const f32x4_t& v) {

@@ -529,9 +529,8 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
         }
         if (whole) {
           const int32_t qi = fastdiv(pr, a.group), qj = pr - qi * a.g;
-          const float inv = sum == 0.0f ? 0.0f : ts_v / sum;
           store_out4<BF16>(a.out + ((int64_t)(w.first + qi) * a.q_heads + (hg * a.hw + h) * a.g + qj) * kD + 4 * d4,
-                           acc * inv);
+                           finish(acc, sum, ts_v));
         } else {
           const int at = (h * RT + rt) * 16 + r;
           *reinterpret_cast<f32x4_t*>(part + (int64_t)at * kD + 4 * d4) = acc;
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(THREADS) kv_attend_join_kernel(AttendArgs a, i
     for (int i = 0; i < THREADS / 64; ++i) sum += red[1][i];
     for (int i = 1; i < groups; ++i) x += acc[i * quads + d4];
     const float ts = ts_p ? *ts_p : 1.0f;
-    store_out4<BF16>(a.out + (r * a.q_heads + qh) * head_dim + 4 * d4, x * (sum == 0.0f ? 0.0f : ts / sum));
+    store_out4<BF16>(a.out + (r * a.q_heads + qh) * head_dim + 4 * d4, finish(x, sum, ts));
   }
 }
 

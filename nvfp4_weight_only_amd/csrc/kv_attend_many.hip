@@ -533,14 +533,13 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
       const int32_t row_now = pr0 + col_now;
       if (row_now < w.packed) {
         const int32_t i = fastdiv(row_now, a.group), j = row_now - i * a.g;
-        const float inv = l == 0.0f ? 0.0f : ts_v / l;
         uint16_t* out = a.out + ((int64_t)(w.first + i) * a.q_heads + head * a.g + j) * kD + 4 * half_now;
 #pragma unroll
         for (int d = 0; d < NS; ++d)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const f32x4_t v = {o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]};
-            store_out4<BF16>(out + 32 * d + 8 * k, v * inv);
+            store_out4<BF16>(out + 32 * d + 8 * k, finish(v, l, ts_v));
           }
       }
     } else if (wave_live) {
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
 template <bool BF16, int NS>
 __global__ void __launch_bounds__(256) kv_attend_many_join_kernel(AttendArgs a, ManyPlan p, const float* ts_p) {
   using M = Many<NS>;
-  __shared__ float weight[32], best[32];
+  __shared__ float total_of[32], best[32];
   const int32_t item = blockIdx.x / M::kWaves, wave = blockIdx.x % M::kWaves, head = blockIdx.y;
   if (item >= (int32_t)p.head[0]) return;
   const int64_t units = p.head[1], total = units * a.c.heads;
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(256) kv_attend_many_join_kernel(AttendArgs a, 
   for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d, 64);
   if (lead == 0) {
     best[row] = mm_row;
-    weight[row] = sum == 0.0f ? 0.0f : ts / sum;
+    total_of[row] = sum;
   }
   __syncthreads();
   const float mm = best[r];
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(256) kv_attend_many_join_kernel(AttendArgs a, 
   const int32_t qi = fastdiv(pr, a.group), qj = pr - qi * a.g;
   uint16_t* out = a.out + ((int64_t)(w.first + qi) * a.q_heads + head * a.g + qj) * M::kD + 4 * (lane >> 5);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) store_out4<BF16>(out + 8 * (quarter * NS + i), acc[i] * weight[r]);
+  for (int i = 0; i < NS; ++i) store_out4<BF16>(out + 8 * (quarter * NS + i), finish(acc[i], total_of[r], ts));
 }
 
 int64_t many_tiles(int64_t rows, int64_t g, int64_t seqs, int64_t tile) {

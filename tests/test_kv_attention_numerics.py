@@ -101,3 +101,22 @@ def test_infinite_queries(nv, shape, dt, fmt):
         assert np.isnan(got[sees, 1]).all() and (got[~sees, 1] == 0).all()
         others = [0, *range(2, g)]
         assert np.array_equal(got[:, others], clean[:, others])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_tiny_value_scales(nv, shape):
+    """A value tensor scale whose quotient by the sum of many weights is below FP32's range, while the outputs are not:
+    sequences within a workgroup's share, and one that is joined."""
+    per, g = shape
+    rng = np.random.default_rng(503)
+    lens = [600] * 150 + [30000]
+    nb, table, lens, start = make_batch(rng, lens, [per] * 151, 64)
+    c = make_cache(rng, "nvfp4", nb, 64, 1, 64)
+    c["v_codes"] = rng.integers(1, 8, size=c["v_codes"].shape, dtype=np.uint8) * np.uint8(17)
+    c["v_scales"][:] = 0x60
+    c["v_tscale"] = np.float32(2.0 ** -130)
+    cache = device_cache(nv, "nvfp4", c)
+    q = rand(rng, (151 * per, g, 64), torch.bfloat16)
+    got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=0.001)
+    within(got, q, c, "nvfp4", table, lens, start, 0.001, 0, 2.0 ** -11)
