@@ -657,7 +657,9 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * query is (or is off by less than 2^-25 of its row's largest element), the weights w_t are
  * rounded to 22 significant bits with NVFP4 (to 2^-32 of the largest where that is more; to 11
  * bits for BF16 outputs where a sequence has many rows) and to 16 with MXFP4 (those below
- * 2^-118 of the largest may be 0).
+ * 2^-118 of the largest may be 0).  Scores of 2^128 and more, and MXFP4 values
+ * with n |v_t| of 2^128 and more over the n tokens that a row sees, pass FP32's range: such a
+ * row's outputs are infinite, NaN or unspecified.
  * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
  * rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
  * NVFP4_ERR_UNSUPPORTED).

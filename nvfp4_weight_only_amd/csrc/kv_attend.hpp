@@ -43,8 +43,9 @@ constexpr uint32_t kMxNan = 253;
 // maximum.  FP16: bias 7, so up to 2^15, its last power of two: a weight 2^21 below the
 // largest is still a normal number, and below that it is off by at most 2^-32 of the
 // largest (without the bias by 2^-25, which 10^5 small weights add up to something seen).
-// BF16 has FP32's range: bias -8, so up to 1, and sums of large MXFP4 values stay in range
-// as long as the result does.  Sums keep the bias; it cancels in the quotient.
+// BF16 has FP32's range: bias -8, so up to 1, as a softmax's own, and the sum over n tokens
+// of MXFP4 values v stays in range while n |v| is below 2^128 (a lower bias would allow more
+// and lose small weights instead).  Sums keep the bias; it cancels in the quotient.
 constexpr float kSlack = 8.0f;
 template <bool MX>
 constexpr float weight_bias() {

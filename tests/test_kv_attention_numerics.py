@@ -120,3 +120,27 @@ def test_tiny_value_scales(nv, shape):
     q = rand(rng, (151 * per, g, 64), torch.bfloat16)
     got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=0.001)
     within(got, q, c, "nvfp4", table, lens, start, 0.001, 0, 2.0 ** -11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_sums_of_large_mxfp4_values(nv, shape):
+    """500 tokens of 6 * 2^116, n |v| = 2^127.55, the first of them with a score just below the step at which the maximum
+    is taken again, so that the others' weights are the largest that there are."""
+    per, g = shape
+    rng = np.random.default_rng(504)
+    n = 500
+    nb, table, lens, start = make_batch(rng, [n, n], [per, per], 16)
+    c = make_cache(rng, "mxfp4", nb, 16, 1, 64)
+    c["k_codes"][:], c["k_scales"][:] = 0x22, 127                 # 1.0
+    c["v_scales"][:] = 243
+    c["v_codes"] = np.broadcast_to(rng.choice(np.array([0x77, 0xFF], np.uint8), size=(1, 1, 1, 32)), c["v_codes"].shape).copy()
+    for s in range(2):
+        for t in range(32):
+            c["k_codes"][table[s, t // 16], t % 16] = 0
+    cache = device_cache(nv, "mxfp4", c)
+    q = torch.ones((2 * per, g, 64), dtype=torch.bfloat16, device="cuda")
+    scale = 7.9 * np.log(2) / 64
+    got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale)
+    within(got, q, c, "mxfp4", table, lens, start, np.float64(np.float32(scale)), 0, 2.0 ** -16)
+    assert (f64(got) == K.values("mxfp4", c["v_codes"][table[0, 0], 0], c["v_scales"][table[0, 0], 0])).all()
