@@ -668,10 +668,11 @@ def _call(fn, what: str, device: torch.device, *args) -> None:
 
 
 def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    device = first.device
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return first.device
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+    return device
 
 
 def _fp8_blocks(n: int) -> int:
@@ -886,19 +887,54 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
     return freqs
 
 
+_DATA_PTR = torch.Tensor.data_ptr
+
+
+class _RopeNow:
+    """A rotation's C struct, its address, and that of the frequencies when it was made."""
+    __slots__ = ("at", "struct", "ref", "rot_dim")
+
+    def __init__(self, at: int, struct: _RopeStruct, rot_dim: int):
+        self.at, self.struct, self.ref, self.rot_dim = at, struct, ctypes.addressof(struct), rot_dim
+
+
+class _CacheNow:
+    """A cache's C struct, its address and sizes, and its tensors' addresses when it was made."""
+    __slots__ = ("at", "struct", "ref", "num_blocks", "block_size", "heads", "head_dim")
+
+    def __init__(self, at: Tuple, struct: _KvCacheStruct, sizes: Tuple):
+        self.at, self.struct, self.ref = at, struct, ctypes.addressof(struct)
+        self.num_blocks, self.block_size, self.heads, self.head_dim = sizes
+
+
 class Rope:
     """A position rotation, made once and kept: the first 2 * len(freqs) elements of a head turned by position * freqs
     (float64, radians a token, on the device), pairs (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved, times
-    amplitude."""
+    amplitude.  Its attributes are read-only."""
 
     def __init__(self, freqs: torch.Tensor, amplitude: float = 1.0, interleaved: bool = False):
+        self._freqs, self._amplitude, self._interleaved = freqs, float(amplitude), bool(interleaved)
+        self._made = self._make()
+
+    freqs = property(lambda self: self._freqs)
+    amplitude = property(lambda self: self._amplitude)
+    interleaved = property(lambda self: self._interleaved)
+    rot_dim = property(lambda self: self._made.rot_dim)
+
+    def _make(self) -> "_RopeNow":
+        freqs = self._freqs
         _need(freqs, torch.float64, "freqs")
         if freqs.dim() != 1 or freqs.numel() == 0 or freqs.numel() % 8 != 0:
             raise ValueError("freqs must be [rot / 2], rot a positive multiple of 16")
-        self.freqs, self.amplitude, self.interleaved = freqs, float(amplitude), bool(interleaved)
-        self.rot_dim = 2 * freqs.numel()
-        self._struct = _RopeStruct(freqs.data_ptr(), self.rot_dim, self.amplitude, int(self.interleaved))
-        self._ref = ctypes.addressof(self._struct)
+        at, rot = freqs.data_ptr(), 2 * freqs.numel()
+        return _RopeNow(at, _RopeStruct(at, rot, self._amplitude, int(self._interleaved)), rot)
+
+    def _now(self) -> "_RopeNow":
+        """What the C entry points take, made again if freqs has other memory by now."""
+        now = self._made
+        if now.at != self._freqs.data_ptr():
+            now = self._made = self._make()
+        return now
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: Optional[torch.Tensor] = None,
@@ -911,28 +947,54 @@ def rope(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: Optional[tor
     rows, heads, head_dim = x.shape
     if positions.shape != (rows,):
         raise ValueError("positions must be [rows]")
-    if rope.rot_dim > head_dim:
-        raise ValueError(f"the rotation turns {rope.rot_dim} elements, a head has {head_dim}")
+    turn = rope._now()
+    if turn.rot_dim > head_dim:
+        raise ValueError(f"the rotation turns {turn.rot_dim} elements, a head has {head_dim}")
     if out is not None:
         if _need_heads(out, "out") != code or out.shape != x.shape:
             raise ValueError("out must have x's shape and type")
-    device = _one_device(x, positions, rope.freqs, out)
+    device = _one_device(x, positions, rope._freqs, out)
     if out is None:
         out = torch.empty((rows, heads, head_dim), dtype=x.dtype, device=device)
     _call(lib().nvfp4_rope, "nvfp4_rope", device, code, x.data_ptr(), rows, heads, head_dim, x.stride(0), x.stride(1),
-          positions.data_ptr(), rope._ref, int(inverse), out.data_ptr(), out.stride(0), out.stride(1))
+          positions.data_ptr(), turn.ref, int(inverse), out.data_ptr(), out.stride(0), out.stride(1))
     return out
 
 
 class KVCache:
     """One layer's keys and values in a paged FP4 cache, made once and kept: the tensors that kv_gather takes (codes
     uint8 [num_blocks, block_size, heads, head_dim/2], scales uint8 [..., head_dim/G]; tensor scales float32 [1] for
-    "nvfp4", none for "mxfp4"), for kv_append and kv_attention."""
+    "nvfp4", none for "mxfp4"), for kv_append and kv_attention.  Its attributes are read-only."""
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  k_tscale: Optional[torch.Tensor] = None, v_tscale: Optional[torch.Tensor] = None, fmt: str = "nvfp4"):
         if fmt not in KV_FORMATS:
             raise ValueError(f"unknown KV format {fmt!r}")
+        if fmt == "nvfp4":
+            for t, name in ((k_tscale, "k_tscale"), (v_tscale, "v_tscale")):
+                if t is None:
+                    raise ValueError(f"an NVFP4 cache needs {name}")
+            self._memory = (k_codes, k_scales, v_codes, v_scales, k_tscale, v_tscale)
+        else:
+            self._memory = (k_codes, k_scales, v_codes, v_scales)
+        self._fmt = fmt
+        self._made = self._make()
+
+    k_codes = property(lambda self: self._memory[0])
+    k_scales = property(lambda self: self._memory[1])
+    v_codes = property(lambda self: self._memory[2])
+    v_scales = property(lambda self: self._memory[3])
+    k_tscale = property(lambda self: self._memory[4] if self._fmt == "nvfp4" else None)
+    v_tscale = property(lambda self: self._memory[5] if self._fmt == "nvfp4" else None)
+    fmt = property(lambda self: self._fmt)
+    device = property(lambda self: self._memory[0].device)
+    num_blocks = property(lambda self: self._made.num_blocks)
+    block_size = property(lambda self: self._made.block_size)
+    heads = property(lambda self: self._made.heads)
+    head_dim = property(lambda self: self._made.head_dim)
+
+    def _make(self) -> "_CacheNow":
+        fmt, (k_codes, k_scales, v_codes, v_scales), tscales = self._fmt, self._memory[:4], self._memory[4:]
         for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
             _need(t, torch.uint8, name)
             if t.dim() != 4:
@@ -944,23 +1006,22 @@ class KVCache:
             raise ValueError("v_codes must have k_codes' shape")
         if k_scales.shape != (nb, bs, heads, 2 * half // _KV_GROUP[fmt]) or v_scales.shape != k_scales.shape:
             raise ValueError("scales do not match codes")
-        if fmt == "nvfp4":
-            for t, name in ((k_tscale, "k_tscale"), (v_tscale, "v_tscale")):
-                if t is None:
-                    raise ValueError(f"an NVFP4 cache needs {name}")
-                _need(t, torch.float32, name)
-                if t.numel() != 1:
-                    raise ValueError(f"{name} must be [1]")
-        else:
-            k_tscale = v_tscale = None
-        self.device = _one_device(k_codes, k_scales, v_codes, v_scales, k_tscale, v_tscale)
-        self.k_codes, self.k_scales, self.k_tscale = k_codes, k_scales, k_tscale
-        self.v_codes, self.v_scales, self.v_tscale = v_codes, v_scales, v_tscale
-        self.fmt, self.num_blocks, self.block_size, self.heads, self.head_dim = fmt, nb, bs, heads, 2 * half
-        self._struct = _KvCacheStruct(KV_FORMATS[fmt], nb, bs, heads, 2 * half, k_codes.data_ptr(), k_scales.data_ptr(),
-                                      None if k_tscale is None else k_tscale.data_ptr(), v_codes.data_ptr(),
-                                      v_scales.data_ptr(), None if v_tscale is None else v_tscale.data_ptr())
-        self._ref = ctypes.addressof(self._struct)
+        for t, name in zip(tscales, ("k_tscale", "v_tscale")):
+            _need(t, torch.float32, name)
+            if t.numel() != 1:
+                raise ValueError(f"{name} must be [1]")
+        _one_device(*self._memory)
+        at = tuple(map(_DATA_PTR, self._memory))
+        kc, ks, vc, vs, kt, vt = at if tscales else (*at, None, None)
+        return _CacheNow(at, _KvCacheStruct(KV_FORMATS[fmt], nb, bs, heads, 2 * half, kc, ks, kt, vc, vs, vt),
+                         (nb, bs, heads, 2 * half))
+
+    def _now(self) -> "_CacheNow":
+        """What the C entry points take, checked and made again if a tensor has other memory by now."""
+        now = self._made
+        if now.at != tuple(map(_DATA_PTR, self._memory)):
+            now = self._made = self._make()
+        return now
 
     @classmethod
     def zeros(cls, num_blocks: int, block_size: int, heads: int, head_dim: int, fmt: str = "nvfp4",
@@ -1007,21 +1068,22 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
     if _need_heads(v, "v") != code:
         raise ValueError("k and v must have the same type")
     rows = k.shape[0]
-    if k.shape[1:] != (cache.heads, cache.head_dim) or v.shape != k.shape:
+    pages, turn = cache._now(), None if rope is None else rope._now()
+    if k.shape[1:] != (pages.heads, pages.head_dim) or v.shape != k.shape:
         raise ValueError("k and v must be [rows, heads, head_dim] of the cache")
     batch = _batch(cache, rows, block_table, seq_lens, row_start)
-    if rope is not None and rope.rot_dim > cache.head_dim:
-        raise ValueError(f"the rotation turns {rope.rot_dim} elements, a head has {cache.head_dim}")
+    if turn is not None and turn.rot_dim > pages.head_dim:
+        raise ValueError(f"the rotation turns {turn.rot_dim} elements, a head has {pages.head_dim}")
     if positions is not None:
         if rope is None:
             raise ValueError("positions need a rope")
         _need(positions, torch.int32, "positions")
         if positions.shape != (rows,):
             raise ValueError("positions must be [rows]")
-    device = _one_device(cache.k_codes, k, v, block_table, seq_lens, row_start, positions,
-                         None if rope is None else rope.freqs)
-    _call(lib().nvfp4_kv_append, "nvfp4_kv_append", device, cache._ref, code, k.data_ptr(), v.data_ptr(), rows,
-          k.stride(0), k.stride(1), v.stride(0), v.stride(1), *batch, None if rope is None else rope._ref,
+    device = _one_device(cache._memory[0], k, v, block_table, seq_lens, row_start, positions,
+                         None if rope is None else rope._freqs)
+    _call(lib().nvfp4_kv_append, "nvfp4_kv_append", device, pages.ref, code, k.data_ptr(), v.data_ptr(), rows,
+          k.stride(0), k.stride(1), v.stride(0), v.stride(1), *batch, None if turn is None else turn.ref,
           None if positions is None else positions.data_ptr())
 
 
@@ -1045,7 +1107,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
     uint8 device tensor of at least kv_attention_workspace_bytes(...) bytes; allocated when it is not given."""
     code = _need_heads(q, "q")
     rows, q_heads, head_dim = q.shape
-    if head_dim != cache.head_dim or q_heads == 0 or q_heads % cache.heads != 0:
+    pages = cache._now()
+    if head_dim != pages.head_dim or q_heads == 0 or q_heads % pages.heads != 0:
         raise ValueError("q must be [rows, q_heads, head_dim], q_heads a multiple of the cache's heads")
     batch = _batch(cache, rows, block_table, seq_lens, row_start)
     if window is None:
@@ -1056,15 +1119,15 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
         _need(out, q.dtype, "out")
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    need = kv_attention_workspace_bytes(cache.heads, head_dim, q_heads, rows, batch[-1])
+    need = kv_attention_workspace_bytes(pages.heads, head_dim, q_heads, rows, batch[-1])
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    device = _one_device(cache.k_codes, q, block_table, seq_lens, row_start, out, workspace)
+    device = _one_device(cache._memory[0], q, block_table, seq_lens, row_start, out, workspace)
     if out is None:
         out = torch.empty((rows, q_heads, head_dim), dtype=q.dtype, device=device)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _call(lib().nvfp4_kv_attention, "nvfp4_kv_attention", device, cache._ref, code, q.data_ptr(), rows, q_heads,
+    _call(lib().nvfp4_kv_attention, "nvfp4_kv_attention", device, pages.ref, code, q.data_ptr(), rows, q_heads,
           q.stride(0), q.stride(1), *batch, head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return out
