@@ -1115,6 +1115,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
         window = 0
     elif window <= 0:
         raise ValueError("window must be positive")
+    else:
+        window = min(window, 2 ** 31 - 1)  # longer than any sequence
     if out is not None:
         _need(out, q.dtype, "out")
         if out.shape != q.shape:

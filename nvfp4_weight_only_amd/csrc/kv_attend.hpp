@@ -28,6 +28,7 @@
 #pragma once
 
 #include "kv_common.hpp"
+#include "kv_masks.hpp"
 
 namespace nvfp4 {
 
@@ -173,16 +174,6 @@ __device__ __forceinline__ u32x4v_t decode8_mx(uint32_t w, float s) {
                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 }
 
-// Bits 0 .. n - 1.
-__device__ __forceinline__ uint32_t low_bits(int32_t n) {
-  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
-}
-// Of the 32 tokens from t0 on, those that a row at position pos sees by its place.
-__device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t window, int32_t t0) {
-  const uint32_t to = low_bits(pos - t0 + 1);
-  return window > 0 ? to & ~low_bits(pos - window - t0 + 1) : to;
-}
-
 // A lane's quarter of a cache row: NS pieces of 8.
 template <bool MX, int NS>
 __device__ __forceinline__ void decode_quarter(const uint32_t (&w)[NS], uint32_t sw, int quarter, u32x4v_t (&out)[NS]) {
@@ -255,7 +246,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int32_t s) {
   const int64_t p0 = r.first + r.shift, p1 = p0 + r.count;
   w.pos = p0 < -a.b.rows ? -(int32_t)a.b.rows : (int32_t)p0;  // every row of such a sequence is below token 0
   w.hi = (int32_t)(p1 < 0 ? 0 : (p1 < r.len ? p1 : r.len));
-  w.lo = a.window > 0 && p0 - a.window + 1 > 0 ? (int32_t)(p0 - a.window + 1) & ~31 : 0;
+  w.lo = first_tile(p0, a.window, 32, w.hi);
   w.rtiles = (w.packed + ROWS - 1) / ROWS;
   // A sequence whose rows see nothing still has its zeros to write.
   w.ttiles = w.hi > w.lo ? fastdiv(w.hi - w.lo + a.unit.d - 1, a.unit) : 1;

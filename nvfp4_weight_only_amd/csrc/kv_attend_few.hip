@@ -306,7 +306,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
     const int32_t in_tile = w.packed - rtile * kRows < kRows ? w.packed - rtile * kRows : kRows;
     const int32_t all_pos = w.pos + fastdiv(rtile * kRows, a.group);
     const int32_t last_pos = w.pos + fastdiv(rtile * kRows + in_tile - 1, a.group);
-    const int32_t all_first = a.window > 0 && last_pos >= a.window ? last_pos - a.window + 1 : 0;
+    const int32_t all_first = first_seen(last_pos, a.window);
 
     // Loads that four neighbouring lanes make of one row reach the cache as one access, in the products' order they would
     // be four (16 streams of up to 8192 tokens: 28.8 instead of 31.8 us); a key's pieces change lanes afterwards.
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
       const uint32_t there = here;
       const bool masked = there != 0xFFFFFFFFu || tb + 31 > all_pos || tb < all_first;
       const auto seen = [&](int rt, int t) {
-        return ((there >> t) & 1u) && tb + t <= pos[rt] && (a.window == 0 || tb + t > pos[rt] - a.window);
+        return ((there >> t) & 1u) && sees(pos[rt], a.window, tb + t);
       };
       const bool more = tile + 1 < mine;
       if (more) place();

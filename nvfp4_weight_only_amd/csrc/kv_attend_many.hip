@@ -58,7 +58,7 @@ __device__ __forceinline__ Tile tile_of(const AttendArgs& a, const SeqWork& w, i
   t.packed = w.packed;
   t.pos = w.pos;
   t.hi = p1 < w.hi ? (p1 < 0 ? 0 : p1) : w.hi;
-  t.lo = a.window > 0 && p0 >= a.window ? (p0 - a.window + 1) & ~(kManyTokens - 1) : 0;
+  t.lo = first_tile(p0, a.window, kManyTokens, t.hi);
   t.units = t.hi > t.lo ? (t.hi - t.lo + kManyTokens - 1) / kManyTokens : 1;
   return t;
 }
@@ -296,10 +296,10 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
     const int32_t live_end = w.packed < (rtile + 1) * kRows ? w.packed : (rtile + 1) * kRows;
     const int32_t wave_end = live_end < pr0 + 32 ? live_end : pr0 + 32;
     const bool wave_live = pr0 < wave_end;
-    const auto first_of = [&](int32_t p_last) { return a.window > 0 && p_last >= a.window ? p_last - a.window + 1 : 0; };
-    const int32_t tile_pos = pos_of(rtile * kRows), tile_first = first_of(pos_of(live_end - 1));
+    const int32_t tile_pos = pos_of(rtile * kRows), tile_first = first_seen(pos_of(live_end - 1), a.window);
     const int32_t wave_pos = wave_live ? pos_of(pr0) : 0, wave_last = wave_live ? pos_of(wave_end - 1) : -1;
-    const int32_t wave_first = wave_live ? first_of(wave_last) : 0, wave_low = wave_live ? first_of(wave_pos) : 0;
+    const int32_t wave_first = wave_live ? first_seen(wave_last, a.window) : 0;
+    const int32_t wave_low = wave_live ? first_seen(wave_pos, a.window) : 0;
 
     // Unit u's quarters into its buffer.
     const auto decode = [&](int32_t u) {
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
     uint32_t th[2];     // of the unit whose scores are in s: its tokens that are in the cache
     uint32_t nan_any;  // whether NaN blocks were taken out of its values
     const auto seen = [&](int32_t tb, int t) {
-      return ((th[t >> 5] >> (t & 31)) & 1u) && tb + t <= pos && (a.window == 0 || tb + t > pos - a.window);
+      return ((th[t >> 5] >> (t & 31)) & 1u) && sees(pos, a.window, tb + t);
     };
     f32x16_t s[2];  // register e of s[t] is token 32 t + 8 (e / 4) + 4 half + e % 4
     u32x4v_t pf[kWeightTerms][4];

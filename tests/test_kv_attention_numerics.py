@@ -144,3 +144,25 @@ def test_sums_of_large_mxfp4_values(nv, shape):
     got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale)
     within(got, q, c, "mxfp4", table, lens, start, np.float64(np.float32(scale)), 0, 2.0 ** -16)
     assert (f64(got) == K.values("mxfp4", c["v_codes"][table[0, 0], 0], c["v_scales"][table[0, 0], 0])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [FEW, MANY, (9, 16)], ids=["few", "many", "more"])
+def test_widest_windows(nv, shape):
+    """Windows up to 2^31 - 1 (and beyond, which the binding takes as that), rows before token 0 among those that they
+    let see; lengths far behind the table, whose rows see its end through a long window and nothing through a short one."""
+    per, g = shape
+    rng = np.random.default_rng(505)
+    lens = [per - 1 if per > 1 else 0, 3, 40, 200]
+    nb, table, lens, start = make_batch(rng, lens, [per] * 4, 16)
+    c = make_cache(rng, "nvfp4", nb, 16, 1, 64)
+    cache = device_cache(nv, "nvfp4", c)
+    q = rand(rng, (4 * per, g, 64), torch.bfloat16)
+    plain = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start))
+    within(plain, q, c, "nvfp4", table, lens, start, 0.125, 0, 2.0 ** -11)
+    for window in (2 ** 30, 2 ** 31 - 5, 2 ** 31 - 1, 2 ** 40, 2 ** 70):
+        assert torch.equal(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), window=window), plain)
+    far = np.array([2 ** 31 - 1, 2 ** 31 - 40, 10 ** 6, 300], np.int64)
+    for window in (7, 100, 2 ** 31 - 1):
+        got = nv.kv_attention(q, cache, i32(table), i32(far), i32(start), window=window)
+        within(got, q, c, "nvfp4", table, far, start, 0.125, window, 2.0 ** -11)
