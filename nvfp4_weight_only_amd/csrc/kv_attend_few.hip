@@ -31,17 +31,19 @@ namespace {
 
 constexpr int kFewTokens = 32;
 
-// Sizes by head dimension, rows and terms.  One workgroup a CU, of 12 wavefronts where 168
-// registers do (16 would spill, and what a wavefront does once, some 800 instructions, counts
-// for each: 40 us for 16 streams of up to 8192 tokens instead of 32; 8 wavefronts 31, and one
-// stream of 131072 46 instead of 42), else 8.
+// One workgroup a CU, of 12 wavefronts where 168 registers do (16 would spill, and what a wavefront does once, some 800
+// instructions, counts for each: 40 us for 16 streams of up to 8192 tokens instead of 32; 8 wavefronts 31, and one
+// stream of 131072 46 instead of 42), else 8.  ns: head dimension / 32, rt: 16-row tiles.
+constexpr int few_waves(int ns, int rt) { return ns == 8 ? 6 : (ns * rt <= 4 ? 12 : 8); }
+// Heads of a workgroup, at most.  4: lines are shared; with 32 rows 2, for smaller parts (8 x 4 rows of 32 heads on 4,
+// window 4096: 27.6 us and join 6.5 with 2, 29.6 and 7.4 with 4; 16 rows, 16 streams of up to 8192: 33.6 and 29.3).
+constexpr int few_heads(int ns, int rt) { return ns == 8 || rt == 2 ? 2 : 4; }
+
+// Sizes by head dimension, rows and terms.
 template <int NS, int RT, int TERMS>
 struct Few {
   static constexpr int kD = 32 * NS, kRows = 16 * RT;
-  static constexpr int kWaves = NS == 8 ? 6 : (NS * RT <= 4 ? 12 : 8);
-  // Heads of a workgroup, at most.  4: lines are shared; with 32 rows 2, for smaller parts (8 x 4 rows of 32 heads on 4,
-  // window 4096: 27.6 us and join 6.5 with 2, 29.6 and 7.4 with 4; 16 rows, 16 streams of up to 8192: 33.6 and 29.3).
-  static constexpr int kHeads = NS == 8 || RT == 2 ? 2 : 4;
+  static constexpr int kWaves = few_waves(NS, RT), kHeads = few_heads(NS, RT);
   static constexpr bool kQInLds = NS * RT * TERMS > 4;       // queries: more than 16 registers
   // LDS: 32 tokens' values a wavefront, rows 32 bytes longer than the values, so that 8 rows start in different banks, and of
   // tokens 8-15 every two 16-byte pieces change places, so that a write's 16 rows use all of them;
@@ -678,7 +680,7 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
   FewPlan p;
   p.rt = rows * (q_heads / heads) > 16 * seqs && head_dim <= 128 ? 2 : 1;
   const int ns = (int)(head_dim / 32);
-  const int waves = ns == 8 ? 6 : (ns * p.rt <= 4 ? 12 : 8), most = ns == 8 || p.rt == 2 ? 2 : 4;
+  const int waves = few_waves(ns, p.rt), most = few_heads(ns, p.rt);
   const int64_t groups = (heads + most - 1) / most;
   p.hw = (int)((heads + groups - 1) / groups);
   p.hgroups = (int)((heads + p.hw - 1) / p.hw);
