@@ -660,8 +660,11 @@ nvfp4_status nvfp4_rope(int type, const uint16_t* x, int64_t rows, int64_t heads
  * 2^-118 of the largest may be 0).  Scores of 2^128 and more, and MXFP4 values
  * with n |v_t| of 2^128 and more over the n tokens that a row sees, pass FP32's range: such a
  * row's outputs are infinite, NaN or unspecified.
- * Results are the same bits on every run.  scale finite; head_dim 64, 96, 128, 192 or 256 and
- * rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
+ * The same call gives the same bits on every run.  A row's last bits do depend on the rest of
+ * the call: its rows (those of no sequence too) and sequences choose between a kernel for few
+ * and one for many rows, and with the heads, the lengths and max_blocks how a sequence's tokens
+ * are shared and in which order its parts are added.  scale finite; head_dim 64, 96, 128, 192 or
+ * 256 and rows * q_heads at most 2^28, and num_blocks * block_size * heads at most 2^30 (others
  * NVFP4_ERR_UNSUPPORTED).
  * Workspace: nvfp4_kv_attention_workspace_bytes bytes (-1: invalid or unsupported shape; no
  * HIP call), any contents, overlapping no argument, not shared by calls in flight at the same

@@ -553,7 +553,9 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
 
 // Joins the parts of one row and query head, if its tokens were shared: their maxima,
 // sums and outputs.  A thread loads every part of its 4 elements that it adds at once;
-// the order of the sums depends on the number of parts alone.
+// the order of the sums is fixed by the number of parts, the head dimension and THREADS,
+// which launch_few takes by the rows, heads and width of the table: no atomics, so the same
+// call gives the same bits.
 constexpr int kJoinParts = 256;  // workgroups at most
 
 template <bool BF16, int ROWS, int THREADS>
