@@ -81,3 +81,60 @@ def test_far_mxfp4_scales(nv, dt, shape):  # noqa: F811
         scale = float(np.float32(0.125 / size))
         got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale)
         within(got, q, c, "mxfp4", table, lens, start, scale, 0, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("rows, g, d", [(40, 8, 128), (40, 8, 256), (12, 4, 64)], ids=["many", "many256", "few"])
+def test_captured_with_other_lengths(nv, rows, g, d, fmt):  # noqa: F811
+    """Two graphs that share a workspace, replayed in turn with lengths and chunks that change in between: rows move from
+    one sequence to another and some belong to none."""
+    rng = np.random.default_rng(730)
+    table = i32(rng.permutation(96).reshape(3, 32))
+    cache = device_cache(nv, fmt, make_cache(rng, fmt, 96, 16, 2, d))
+    q = [rand(rng, (rows, 2 * g, d), torch.bfloat16) for _ in range(2)]
+    lens, start = i32([100, 200, 300]), i32([0, 3, 4, rows])
+    ws = torch.empty(nv.kv_attention_workspace_bytes(2, d, 2 * g, rows, 3), dtype=torch.uint8, device="cuda")
+    out = [torch.zeros_like(x) for x in q]
+
+    def call(i, out):
+        return nv.kv_attention(q[i], cache, table, lens, start, window=150, out=out, workspace=ws)
+    for i in range(2):
+        call(i, out[i])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            call(i, out[i])
+    for lens_now, start_now in (([100, 200, 300], [0, 3, 4, rows]), ([512, 1, 40], [0, rows - 2, rows - 1, rows]),
+                                ([7, 0, 511], [2, 5, 5, rows - 4]), ([90, 500, 8], [0, 0, rows - 1, rows - 1])):
+        lens.copy_(i32(lens_now))
+        start.copy_(i32(start_now))
+        for x in q:
+            x.copy_(rand(rng, x.shape, x.dtype))
+        for x in out:
+            x.fill_(5.0)
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(out[i], call(i, torch.full_like(q[i], 5.0)))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_heads_outside_rows_and_shared_by_rows(nv, fmt):  # noqa: F811
+    """Keys with heads outside rows, one value head for all, queries with heads outside rows: strides that are allowed."""
+    rng = np.random.default_rng(740)
+    heads, g, d = 3, 5, 96
+    for lens, n in (([60, 33], [1, 1]), ([200, 77], [50, 20])):
+        nb, table, lens, start = make_batch(rng, lens, n, 24)
+        c = make_cache(rng, fmt, nb, 24, heads, d)
+        cache = device_cache(nv, fmt, c)
+        rows = int(start[-1])
+        k = rand(rng, (heads, rows, d), torch.bfloat16).transpose(0, 1)
+        v = rand(rng, (rows, 1, d), torch.bfloat16).expand(rows, heads, d)
+        nv.kv_append(k, v, cache, i32(table), i32(lens), i32(start))
+        c = test_kv_ops.K.append(fmt, c, test_kv_ops.f64(k), test_kv_ops.f64(v), table, lens, start)
+        test_kv_ops.same_cache(test_kv_ops.host_cache(cache, c), c)
+        q = rand(rng, (heads * g, rows, d), torch.float16).transpose(0, 1)
+        got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start))
+        within(got, q, c, fmt, table, lens, start, d ** -0.5, 0, 2.0 ** -22 if fmt == "nvfp4" else 2.0 ** -16)
