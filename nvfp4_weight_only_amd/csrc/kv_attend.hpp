@@ -21,8 +21,8 @@
 // rounding stays far below the output's: with one, the distance from the exact result grew
 // by a quarter to a third for FP16 outputs of NVFP4 and BF16 ones of MXFP4 (9 streams with a
 // chunk of 256 rows: 2.67e-4 instead of 2.07e-4, 2.12e-3 instead of 1.66e-3 of the
-// outputs' norm).  The second term costs 1.2 of 34 us at 16 streams of up to 8192 tokens,
-// where memory bounds, and 100 of 330 at 2048 rows behind 6144 (MXFP4, BF16), where products
+// outputs' norm).  The second term takes 1.5 of 36 us at 16 streams of up to 8192 tokens,
+// where memory bounds, and 80 of 410 at 2048 rows behind 6144 (MXFP4, BF16), where products
 // do; so many rows of NVFP4 with BF16 outputs keep one, 11 bits under an output of 8 (1.669e-3
 // and 1.660e-3).
 #pragma once

@@ -16,11 +16,11 @@
 // up 4 tokens of a column.  A lane then holds scores, statistics and outputs of one row
 // (lane % 16), and the maximum is exchanged only where it has grown by kSlack.
 //
-// Measured (40 query heads on 8 of 128): 16 single rows of up to 8192 tokens (85 MB of
-// NVFP4) 26 us and the join 5.4; in the loop over units the cache comes at 5.8 TB/s (a
-// plain read reaches 7.1), the rest is finding the share, the first loads and joining the
-// slices.  One row of 131072 tokens (143 MB of MXFP4, FP16 outputs: twice the products) 34
-// and 7 us; one of 1000 tokens 9.8 and 5.2.
+// Measured (40 query heads on 8 of 128; medians in a trace): 16 single rows of up to 8192
+// tokens (85 MB of NVFP4) 29.1 us and the join 5.5, 2.9 TB/s over the kernel (a plain read
+// reaches 7.1): beside the loop over units stand finding the share, the first loads and
+// joining the slices.  One row of 131072 tokens (143 MB of MXFP4, FP16 outputs: twice the
+// score products) 34.8 and 7.2 us; one of 1000 tokens 10.8 and 4.6.
 #include <type_traits>
 
 #include "kv_attend.hpp"
@@ -32,11 +32,11 @@ namespace {
 constexpr int kFewTokens = 32;
 
 // One workgroup a CU, of 12 wavefronts where 168 registers do (16 would spill, and what a wavefront does once, some 800
-// instructions, counts for each: 40 us for 16 streams of up to 8192 tokens instead of 32; 8 wavefronts 31, and one
-// stream of 131072 46 instead of 42), else 8.  ns: head dimension / 32, rt: 16-row tiles.
+// instructions, counts for each), else 8.  With the join, 12 and 8: 16 streams of up to 8192 tokens 35.9 and 36.6 us, one
+// of 131072 43.9 and 46.0, one of 1000 14.9 and 13.4.  ns: head dimension / 32, rt: 16-row tiles.
 constexpr int few_waves(int ns, int rt) { return ns == 8 ? 6 : (ns * rt <= 4 ? 12 : 8); }
-// Heads of a workgroup, at most.  4: lines are shared; with 32 rows 2, for smaller parts (8 x 4 rows of 32 heads on 4,
-// window 4096: 27.6 us and join 6.5 with 2, 29.6 and 7.4 with 4; 16 rows, 16 streams of up to 8192: 33.6 and 29.3).
+// Heads of a workgroup, at most.  4: lines are shared (16 streams of up to 8192 tokens with the join 35.9 us, with 2
+// 38.4); with 32 rows 2, for smaller parts (8 x 4 rows of 32 heads on 4, window 4096: 36.9 us, with 4 39.4).
 constexpr int few_heads(int ns, int rt) { return ns == 8 || rt == 2 ? 2 : 4; }
 
 // Sizes by head dimension, rows and terms.
@@ -656,8 +656,8 @@ void launch_few(AttendArgs a, bool bf16, hipStream_t s) {
   }
   const float* ts = a.c.mx ? nullptr : a.c.tscale[1];
   // 1024 threads take 256 parts of 128 elements at once; with a workgroup a CU and more, or sequences too short for many
-  // parts, 256 threads start sooner (with 512 in place of either: 16 rows of 40 heads 7.4 instead of 5.6 us, 1 row of 256
-  // parts 9.4 instead of 7.1; 1 row of 32 parts 5.2 us with 256 threads, 6.1 with 1024).
+  // parts, 256 threads start sooner (both kernels, 256 and 1024 threads: 16 rows of 40 heads 35.9 and 44.0 us, 1 row of
+  // 1000 tokens 14.9 and 16.5, 1 row of 256 parts 45.2 and 43.9).
   const int dim32 = (int)a.c.head_dim;
   const auto join = [&](auto threads, auto bf) {
     constexpr int kThreads = decltype(threads)::value;
@@ -695,9 +695,10 @@ FewPlan few_plan(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows,
 }  // namespace
 
 // Many rows or few, by the packed rows (rows times query heads of a key/value head) of a sequence on average: with 32 (8
-// sequences of up to 16384 tokens, 4 rows each, 32 heads on 4) 34 us by the kernel for few and 47 by the one for many;
-// with 235 (264 rows of 9 sequences, one a chunk, the others single tokens, 16 heads of 256 on 2) 71 by few, 50 by many;
-// with 4092 (7161 rows of 7 prompts, 16 heads of 64 on 4) 419 by few, 96 by many.
+// sequences of up to 16384 tokens, 4 rows each, 32 heads on 4) 37 us by the kernel for few and 44 by the one for many;
+// with 235 (264 rows of 9 sequences, one a chunk, the others single tokens, 16 heads of 256 on 2) 69 by few, 53 by many;
+// with 4092 (7161 rows of 7 prompts, 16 heads of 64 on 4) 403 by few, 94 by many.  Where they cross between 32 and 235 was
+// not looked for.
 static bool many_rows(int64_t g, int64_t rows, int64_t seqs) { return rows * g > 32 * seqs; }
 
 int64_t kv_attend_workspace_bytes(int64_t heads, int64_t head_dim, int64_t q_heads, int64_t rows, int64_t seqs) {
