@@ -47,7 +47,20 @@ constexpr uint32_t kMxNan = 253;
 // BF16 has FP32's range: bias -8, so up to 1, as a softmax's own, and the sum over n tokens
 // of MXFP4 values v stays in range while n |v| is below 2^128 (a lower bias would allow more
 // and lose small weights instead).  Sums keep the bias; it cancels in the quotient.
+//
+// From kFar on FP32's step is half a unit and more: there a step of 8, the bias beside the
+// maximum and the product with the row's factor would each be rounded by so much that weights
+// pass 2^15 (scores of 2^24 and more gave infinite weights in FP16).  A wavefront with such a
+// maximum takes the differences from it first, rounded products on both sides, which are at
+// most 0, and scales again whenever it grows.
 constexpr float kSlack = 8.0f;
+constexpr float kFar = 4194304.0f;  // 2^22
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m > -__builtin_inff(); }
+// A score's difference from a maximum that no score passes; NaN stays.
+__device__ __forceinline__ float below(float score, float m) {
+  const float x = score - (m == -__builtin_inff() ? 0.0f : m);
+  return x > 0.0f ? 0.0f : x;
+}
 template <bool MX>
 constexpr float weight_bias() {
   return MX ? -kSlack : 7.0f;

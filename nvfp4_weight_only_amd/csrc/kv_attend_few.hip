@@ -268,6 +268,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
     u32x4v_t q[RT][kTerms][F::kQInLds ? 1 : NS];
     f32x4_t o[RT][2 * NS];
     float factor[RT], m[RT], l[RT];
+    bool far = false;
     if (F::kQInLds) __syncthreads();  // the buffers' last use, by other wavefronts
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
             if (masked) sc[rt][h][e] = bits & (1u << (16 * h + e)) ? sc[rt][h][e] : -__builtin_inff();
             top = fmaxf(top, sc[rt][h][e]);
           }
-        if (__any(top > m[rt] + kSlack)) {
+        if (__any(top > m[rt] + (far ? 0.0f : kSlack))) {
           top = fmaxf(top, __shfl_xor(top, 16, 64));
           top = fmaxf(top, __shfl_xor(top, 32, 64));
           const float next = fmaxf(m[rt], top);
@@ -426,8 +427,16 @@ __global__ void __launch_bounds__((64 * Few<NS, RT, AttendTerms<MX, BF16, false>
           l[rt] *= shrink;
 #pragma unroll
           for (int d = 0; d < 2 * NS; ++d) o[rt][d] *= shrink;
+          far = far || __any(is_far(next));
         }
-        const float mm = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - weight_bias<MX>();
+        float mm = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - weight_bias<MX>();
+        if (__builtin_expect(far, 0)) {
+          mm = -weight_bias<MX>();
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[rt][h][e] = below(sc[rt][h][e], m[rt]);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float p[4];

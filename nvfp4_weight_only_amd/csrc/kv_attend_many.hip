@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;
+    bool far = false;
 
     // Tokens that every row, of the workgroup's tile and of the wavefront's, sees, and the last that one of the
     // wavefront's sees.
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
       top *= rs.factor;  // positive, or NaN
-      if (__any(top > m + kSlack)) {
+      if (__any(top > m + (far ? 0.0f : kSlack))) {
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float next = fmaxf(m, top);
         const float shrink = next == m ? 1.0f : __builtin_amdgcn_exp2f(m - next);
@@ -397,8 +398,18 @@ __global__ void __launch_bounds__(Many<NS>::kThreads) kv_attend_many_kernel(Atte
         l *= shrink;
 #pragma unroll
         for (int d = 0; d < NS; ++d) o[d] *= shrink;
+        far = far || __any(is_far(next));
       }
-      const float mm = m == -__builtin_inff() ? 0.0f : m - weight_bias<MX>();
+      float mm = m == -__builtin_inff() ? 0.0f : m - weight_bias<MX>();
+      if (__builtin_expect(far, 0)) {
+        // The differences take the scores' place, divided by the factor that the loop below multiplies with.
+        const float inv = 1.0f / rs.factor;
+        mm = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[t][e] = (below(s[t][e] * rs.factor, m) + weight_bias<MX>()) * inv;
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll

@@ -166,3 +166,36 @@ def test_widest_windows(nv, shape):
     for window in (7, 100, 2 ** 31 - 1):
         got = nv.kv_attention(q, cache, i32(table), i32(far), i32(start), window=window)
         within(got, q, c, "nvfp4", table, far, start, 0.125, window, 2.0 ** -11)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_scores_beyond_2_to_the_24(nv, shape, sign, fmt):
+    """Scores of 2^23 to 2^29, where FP32's step is 1 to 64: later tokens lie a little above the first ones' maximum, and
+    the weights' offset from it is rounded.  All values are the same, so that every mean of them is."""
+    per, g = shape
+    rng = np.random.default_rng(506)
+    n, seqs = 1000, 200
+    nb, table, lens, start = make_batch(rng, [n], [per], 16)
+    lens, start = np.repeat(lens, seqs), np.arange(seqs + 1, dtype=np.int32) * per
+    table = np.repeat(table, seqs, 0)
+    c = make_cache(rng, fmt, nb, 16, 1, 64)
+    c["k_codes"][:], c["k_scales"][:] = 0, 0x38 if fmt == "nvfp4" else 127
+    c["k_codes"][..., :16] = 0x77                      # 32 elements of 6 times 2^8
+    c["k_scales"][..., :32 // K.GROUP[fmt]] = 0x78 if fmt == "nvfp4" else 135
+    last = -32 // K.GROUP[fmt]
+    c["k_scales"][..., last:] = 0x10 if fmt == "nvfp4" else 122  # steps of 2^-6
+    for t in range(n):
+        c["k_codes"][table[0, t // 16], t % 16, 0, 16:] = 0 if t < 32 else rng.integers(0, 8, size=16)
+    c["k_tscale"] = c["v_tscale"] = np.float32(1.0) if fmt == "nvfp4" else None
+    c["v_codes"][:], c["v_scales"][:] = np.tile(np.array([0x22, 0x4A], np.uint8), 16), 0x38 if fmt == "nvfp4" else 127
+    cache = device_cache(nv, fmt, c)
+    want = K.values(fmt, c["v_codes"][0, 0], c["v_scales"][0, 0], c["v_tscale"])
+    q = torch.full((seqs * per, g, 64), float(sign), dtype=torch.bfloat16, device="cuda")
+    for power in np.linspace(23, 29, 25):
+        scale = 2.0 ** power / (32 * 1536) / np.log2(np.e)
+        got = f64(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale))
+        wrong = got != want
+        assert not wrong.any(), f"2^{power}: {int(wrong.sum())} wrong, the first of them {got[wrong][:3]}"
