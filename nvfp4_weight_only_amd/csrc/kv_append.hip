@@ -16,7 +16,7 @@
 // neighbouring threads a block; for a rotated key it also loads the piece that holds
 // the other half of its pairs, which a neighbour of the same workgroup loads too.
 //
-// Measured: 2048 rows of 8 heads of 128 (NVFP4) 6.9 us, 16384 (MXFP4) 25 us, 3.4 TB/s.
+// Measured: 2048 rows of 8 heads of 128 (NVFP4) 7.0 us, 16384 (MXFP4) 25 us, 3.4 TB/s.
 // Bound by a workgroup's chain of dependent loads (start, length, page, frequency), which
 // its row loads overlap, and by vector instructions (40 % of the clocks at 16384 rows): 4
 // pieces a thread, 120 registers, 4 wavefronts a SIMD.  With 2 pieces 45 us, with 8 28;

@@ -52,7 +52,8 @@ constexpr uint32_t kMxNan = 253;
 // maximum and the product with the row's factor would each be rounded by so much that weights
 // pass 2^15 (scores of 2^24 and more gave infinite weights in FP16).  A wavefront with such a
 // maximum takes the differences from it first, rounded products on both sides, which are at
-// most 0, and scales again whenever it grows.
+// most 0, and scales again whenever it grows (looking for it takes 1.4 % of the time of 2048
+// rows behind 6144 tokens).
 constexpr float kSlack = 8.0f;
 constexpr float kFar = 4194304.0f;  // 2^22
 __device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m > -__builtin_inff(); }

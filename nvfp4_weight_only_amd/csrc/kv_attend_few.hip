@@ -17,10 +17,10 @@
 // (lane % 16), and the maximum is exchanged only where it has grown by kSlack.
 //
 // Measured (40 query heads on 8 of 128; medians in a trace): 16 single rows of up to 8192
-// tokens (85 MB of NVFP4) 29.1 us and the join 5.5, 2.9 TB/s over the kernel (a plain read
+// tokens (85 MB of NVFP4) 29.9 us and the join 5.5, 2.8 TB/s over the kernel (a plain read
 // reaches 7.1): beside the loop over units stand finding the share, the first loads and
 // joining the slices.  One row of 131072 tokens (143 MB of MXFP4, FP16 outputs: twice the
-// score products) 34.8 and 7.2 us; one of 1000 tokens 10.8 and 4.6.
+// score products) 35.7 and 7.0 us; one of 1000 tokens 10.5 and 4.7.
 #include <type_traits>
 
 #include "kv_attend.hpp"

@@ -17,12 +17,12 @@
 // read the same key/value head's tokens from its L2.
 //
 // Measured: 2048 rows behind 6144 tokens (40 query heads on 8 of 128, 3.0e11 operations;
-// NVFP4 and BF16, one term a weight) 330 to 352 us, 0.9 PFLOP/s (a large library product
-// reaches 1.4), plan 5 and join 17: matrix cores busy 43 % of the clocks, vector instructions
-// 49 %, LDS reads 128 bytes a clock in the phases that multiply.  All three kernels: 340 us,
-// MXFP4 410, FP16 428; MXFP4 and FP16 with two terms of query and weights 561, where heads of
-// 128 spill 40 registers a lane (of 64 none, of 96 17, of 256 18; one term of the query and
-// two of the weights at most 6).
+// NVFP4 and BF16, one term a weight) 360 us, 0.8 PFLOP/s (a large library product reaches
+// 1.4), plan 5 and join 17: matrix cores busy 42 % of the clocks, vector instructions 48 %, LDS
+// reads 128 bytes a clock in the phases that multiply.  All three kernels in a captured graph:
+// 343 us, MXFP4 415, FP16 427; MXFP4 and FP16 with two terms of query and weights 568, where
+// heads of 128 spill 41 registers a lane (of 64 none, of 96 18, of 256 19; one term of the
+// query and two of the weights at most 7).
 #include <type_traits>
 
 #include "kv_attend.hpp"
