@@ -199,3 +199,37 @@ def test_scores_beyond_2_to_the_24(nv, shape, sign, fmt):
         got = f64(nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale))
         wrong = got != want
         assert not wrong.any(), f"2^{power}: {int(wrong.sum())} wrong, the first of them {got[wrong][:3]}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_small_elements_and_small_weights_count(nv, shape, dt, fmt):
+    """Elements of a query 2^-15 of its largest, which meets zeros in the keys; and 20000 weights of 2^-24 of the largest,
+    whose value is 0: subnormal numbers of FP16 on the matrix cores."""
+    per, g = shape
+    dt, rng = TYPES[dt], np.random.default_rng(507)
+    weight = 2.0 ** -16 if fmt == "mxfp4" else 2.0 ** -11
+    nb, table, lens, start = make_batch(rng, [70, 200], [per, per], 16)
+    c = make_cache(rng, fmt, nb, 16, 1, 64)
+    c["k_codes"][..., 0] &= 0xF0                       # element 0
+    cache = device_cache(nv, fmt, c)
+    q = rand(rng, (2 * per, g, 64), dt, 2.0 ** -13)
+    q[..., 0] = 4.0
+    got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=2.0 ** 9)
+    within(got, q, c, fmt, table, lens, start, 2.0 ** 9, 0, weight)
+    n = 20000
+    nb, table, lens, start = make_batch(rng, [n], [per], 64)
+    c = make_cache(rng, fmt, nb, 64, 1, 64)
+    c["k_codes"][:], c["k_scales"][:] = 0, 0x38 if fmt == "nvfp4" else 127
+    c["v_codes"][:], c["v_scales"][:] = 0x22, 0x38 if fmt == "nvfp4" else 127
+    c["k_codes"][table[0, 3], 5] = 0x22                # token 197
+    c["v_codes"][table[0, 3], 5] = 0
+    c["k_tscale"] = c["v_tscale"] = np.float32(1.0) if fmt == "nvfp4" else None
+    cache = device_cache(nv, fmt, c)
+    q = torch.ones((per, g, 64), dtype=dt, device="cuda")
+    scale = 24 * np.log(2) / 64
+    got = nv.kv_attention(q, cache, i32(table), i32(lens), i32(start), scale=scale)
+    within(got, q, c, fmt, table, lens, start, np.float64(np.float32(scale)), 0, weight)
+    assert (np.abs(f64(got) / (n * 2.0 ** -24) - 1) < 0.1).all()
